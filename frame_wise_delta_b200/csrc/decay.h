@@ -1,0 +1,110 @@
+// Decay attention (token-level linear attention with one decay per head):
+// what its kernels and their dispatch share.
+//
+// Every direction is one operator over the tokens of a (batch, head) pair.
+// Walking forward from a state X (value channels x key channels),
+//   X_i = l X_{i-1} + v_i k_i^T,   o_i = X_i q_i,                l = exp(g_h),
+// and walking back from a state Z that has not decayed yet,
+//   Z_i = l Z_{i+1} + v_i k_i^T (Z_last = Z + v k^T),  o_i = Z_i q_i,
+// with l Z_first left behind. The forward pass is the first with (Q, K, V); the backward pass is
+//   dQ: forward with (dO, V, K) from S_in^T,
+//   dK: back with (V, dO, Q) from dS_out^T,    dV: back with (K, Q, dO) from dS_out, leaving dS_in.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "vdn.h"
+
+namespace vdn {
+
+constexpr int kDecayC = 64;      // tokens per chunk of both chunked kernels
+constexpr int kDecayOps = 3;     // operators per launch, at most
+constexpr int kDecayTensors = 7; // Q, K, V, dO and three outputs
+
+// One operator: indexes into DecayArgs.t.
+struct DecayOp {
+  int q, k, v, o;
+  int back;           // walk from the last token to the first
+  int s_in_t;         // s_in is read transposed
+  const float *s_in;  // [BH, d, d] or null (zero)
+  float *s_out;       // [BH, d, d] or null
+};
+
+struct DecayArgs {
+  DecayOp op[kDecayOps];
+  void *t[kDecayTensors];  // [BH, N, d] each
+  const float *g;          // [H]
+  const int32_t *lens;     // [B] or null
+  int32_t *info;           // or null
+  float *ws;               // [nops * BH, nseg, d, d] with nseg > 1
+  long long BH;
+  int H, N, d, nops;
+  int nseg, seglen;        // segments of a sequence; seglen is a multiple of kDecayC
+};
+
+// The split of the sequences over CTAs.
+struct DecaySplit {
+  int nseg, seglen;
+};
+DecaySplit decay_split(long long pairs, long long n);
+
+// What a CTA works on: block -> (operator, b*h, segment).
+struct DecayWork {
+  int op, seg, h, len, begin, end, nch, last_seg;
+  long long bh;
+};
+__device__ __forceinline__ DecayWork decay_work(const DecayArgs &p, long long block) {
+  DecayWork w;
+  w.seg = (int)(block % p.nseg);
+  const long long r = block / p.nseg;
+  w.bh = r % p.BH;
+  w.op = (int)(r / p.BH);
+  w.h = (int)(w.bh % p.H);
+  w.len = p.N;
+  if (p.lens) w.len = min(max(p.lens[w.bh / p.H], 0), p.N);
+  w.begin = min((long long)w.seg * p.seglen, (long long)w.len);
+  w.end = min(((long long)w.seg + 1) * p.seglen, (long long)w.len);
+  w.nch = (w.end - w.begin + kDecayC - 1) / kDecayC;
+  w.last_seg = w.len > 0 ? (w.len - 1) / p.seglen : 0;
+  return w;
+}
+// The segment a walk ends in, and whether a segment lies before it on the way.
+__device__ __forceinline__ int decay_final_seg(const DecayWork &w, int back) { return back ? 0 : w.last_seg; }
+__device__ __forceinline__ bool decay_before_final(const DecayWork &w, int back) {
+  return back ? (w.seg > 0 && w.seg <= w.last_seg) : w.seg < w.last_seg;
+}
+
+// exp(g n) for a whole n >= 0 (g = -inf included), in 64 bits: l^n multiplies
+// a state once per chunk for thousands of chunks, so a power rounded to 32
+// bits would drift by its own error each time.
+__device__ __forceinline__ double decay_pow(float g, long long n) {
+  return n == 0 ? 1.0 : exp((double)g * (double)n);
+}
+
+cudaError_t launch_decay_simt(const DecayArgs &a, int in_dtype, int out_dtype, bool sums, cudaStream_t st);
+cudaError_t launch_decay_prefix(const DecayArgs &a, cudaStream_t st);
+cudaError_t launch_decay_step(const void *Q, const void *K, const void *V, const float *g, const int32_t *active,
+                              const float *s_in, void *O, float *s_out, long long BH, int H, int d, int in_dtype,
+                              int out_dtype, cudaStream_t st);
+
+// One tensor of a rotary call; strides in elements (batch, head, token).
+struct RotaryIo {
+  const void *x;
+  void *y;
+  long long xs[3], ys[3];
+  int rotate;
+};
+constexpr int kRotaryIo = 3;
+constexpr int kRotaryPairs = 64;  // d / 2, at most
+struct RotaryArgs {
+  RotaryIo io[kRotaryIo];
+  int nio, B, H, d, U, gw, interleaved, inverse;
+  long long N, frame0;
+  int npairs[3];              // rotated pairs of each axis
+  const int32_t *pos;         // [B, N, 3] or null
+  double turn[kRotaryPairs];  // turns per position of each pair
+};
+cudaError_t launch_rotary(const RotaryArgs &a, int dtype, cudaStream_t st);
+
+}  // namespace vdn

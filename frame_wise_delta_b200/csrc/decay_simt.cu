@@ -1,0 +1,436 @@
+// Decay attention on the CUDA cores: the chunked form for the types that the
+// tensor-core kernel does not take, the join of the segments' states, and the
+// form for single tokens.
+//
+// Chunked form, per chunk of 64 tokens with local indexes i, j, n valid rows
+// and the state X in front of it (forward walk):
+//   o_i  = sum_{j <= i} l^{i-j} (q_i . k_j) v_j + l^{i+1} X q_i
+//   X'   = l^n X + sum_j l^{n-1-j} v_j k_j^T
+// and on the walk back
+//   o_i  = sum_{j >= i} l^{j-i} (q_i . k_j) v_j + l^{n-1-i} Z q_i
+//   Z'   = l^n Z + sum_j l^{j+1} v_j k_j^T.
+// Powers with whole exponents >= 0 only, each at most 1, so nothing overflows.
+// All sums are in float32; everything outside j <= i or behind the last token
+// is selected away, not multiplied by 0.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "decay.h"
+#include "internal.h"
+
+namespace vdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kC = kDecayC;
+
+template <int D>
+struct SimtSmem {
+  float q[kC][D + 4], k[kC][D + 4], v[kC][D + 4];
+  float st[D][D + 4];  // the state, st[key][value]
+  float p[kC][kC + 4];
+  float pw[kC + 1];    // l^n
+  float carry[2];      // l^n of the chunk's valid rows, as two floats
+};
+
+template <int W>
+__device__ __forceinline__ void lds(const float *p, float (&r)[W]) {
+  if constexpr (W == 4) {
+    const float4 x = *reinterpret_cast<const float4 *>(p);
+    r[0] = x.x, r[1] = x.y, r[2] = x.z, r[3] = x.w;
+  } else if constexpr (W == 2) {
+    const float2 x = *reinterpret_cast<const float2 *>(p);
+    r[0] = x.x, r[1] = x.y;
+  } else {
+    r[0] = p[0];
+  }
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void load_rows(const T *src, int rows, float (*dst)[D + 4]) {
+  constexpr int V = 16 / sizeof(T);
+  for (int e = threadIdx.x; e < kC * (D / V); e += kThreads) {
+    const int r = e / (D / V), c = (e % (D / V)) * V;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < rows) x = *reinterpret_cast<const uint4 *>(src + (long long)r * D + c);
+    const T *y = reinterpret_cast<const T *>(&x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) dst[r][c + i] = to_f32(y[i]);
+  }
+}
+
+// SUMS: only the state that a segment adds (from zero), into the workspace.
+template <typename TI, typename TO, int D, bool SUMS>
+__global__ void __launch_bounds__(kThreads, 1) decay_simt_kernel(const DecayArgs p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SimtSmem<D> &s = *reinterpret_cast<SimtSmem<D> *>(smem_raw);
+  constexpr int VW = D / 16 < 4 ? D / 16 : 4;  // value channels per vector
+  constexpr int NV = D / (16 * VW);            // vectors per thread
+  constexpr int NK = D / 16;                   // key channels per thread of the state
+  const DecayWork w = decay_work(p, blockIdx.x);
+  const DecayOp &op = p.op[w.op];
+  const int back = op.back;
+  if (SUMS && !decay_before_final(w, back)) return;
+  const bool fin = w.seg == decay_final_seg(w, back);
+  if (!SUMS && w.nch == 0 && !fin) return;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  constexpr long long DD = (long long)D * D;
+  const float g = p.g[w.h];
+  if (threadIdx.x <= kC) s.pw[threadIdx.x] = (float)decay_pow(g, threadIdx.x);
+
+  // the state: this thread's key channels ty + 16 a, value channels 16 VW c + VW tx
+  float X[NK][NV * VW];
+  const float *src = nullptr;
+  bool tr = false;
+  if (!SUMS) {
+    if (p.nseg > 1) {
+      src = p.ws + (blockIdx.x) * DD;
+    } else if (op.s_in) {
+      src = op.s_in + w.bh * DD;
+      tr = op.s_in_t;
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < NK; ++a)
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        const int k = ty + 16 * a, v = 16 * VW * c + VW * tx + e;
+        X[a][c * VW + e] = src ? (tr ? src[k * D + v] : src[v * D + k]) : 0.f;
+      }
+
+  const long long base = w.bh * (long long)p.N;
+  for (int it = 0; it < w.nch; ++it) {
+    const int c0 = back ? w.nch - 1 - it : it;
+    const int t0 = w.begin + c0 * kC, n = min(kC, w.end - t0);
+    const long long row = (base + t0) * D;
+    if (!SUMS) load_rows<TI, D>((const TI *)p.t[op.q] + row, n, s.q);
+    load_rows<TI, D>((const TI *)p.t[op.k] + row, n, s.k);
+    load_rows<TI, D>((const TI *)p.t[op.v] + row, n, s.v);
+    if (!SUMS) {
+#pragma unroll
+      for (int a = 0; a < NK; ++a)
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+          for (int e = 0; e < VW; ++e) s.st[ty + 16 * a][16 * VW * c + VW * tx + e] = X[a][c * VW + e];
+    }
+    if (threadIdx.x == 0) {
+      const double l = decay_pow(g, n);
+      s.carry[0] = (float)l;
+      s.carry[1] = (float)(l - (double)(float)l);
+    }
+    __syncthreads();
+    if (!SUMS) {
+      // the scores: rows ty + 16 r, columns tx + 16 c
+      float sc[4][4] = {};
+#pragma unroll 4
+      for (int k = 0; k < D; k += 4) {
+        float a[4][4], b[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) lds<4>(&s.q[ty + 16 * r][k], a[r]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) lds<4>(&s.k[tx + 16 * r][k], b[r]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sc[r][c] = fmaf(a[r][e], b[c][e], sc[r][c]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int i = ty + 16 * r, j = tx + 16 * c, gap = back ? j - i : i - j;
+          s.p[i][j] = gap >= 0 && j < n ? sc[r][c] * s.pw[gap] : 0.f;
+        }
+      __syncthreads();
+      // the outputs: rows 4 ty + r, value channels as the state's
+      float o[4][NV * VW] = {};
+#pragma unroll 2
+      for (int k = 0; k < D; k += 4) {
+        float a[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) lds<4>(&s.q[4 * ty + r][k], a[r]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int c = 0; c < NV; ++c) {
+            float b[VW];
+            lds<VW>(&s.st[k + e][16 * VW * c + VW * tx], b);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int x = 0; x < VW; ++x) o[r][c * VW + x] = fmaf(a[r][e], b[x], o[r][c * VW + x]);
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 4 * ty + r;
+        const float f = i < n ? s.pw[back ? n - 1 - i : i + 1] : 0.f;
+#pragma unroll
+        for (int x = 0; x < NV * VW; ++x) o[r][x] *= f;
+      }
+#pragma unroll 2
+      for (int j = 0; j < kC; j += 4) {
+        float a[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) lds<4>(&s.p[4 * ty + r][j], a[r]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int c = 0; c < NV; ++c) {
+            float b[VW];
+            lds<VW>(&s.v[j + e][16 * VW * c + VW * tx], b);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int x = 0; x < VW; ++x) o[r][c * VW + x] = fmaf(a[r][e], b[x], o[r][c * VW + x]);
+          }
+      }
+      TO *out = (TO *)p.t[op.o] + row;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (4 * ty + r < n) {
+#pragma unroll
+          for (int c = 0; c < NV; ++c)
+#pragma unroll
+            for (int x = 0; x < VW; ++x)
+              store_val(out + (long long)(4 * ty + r) * D + 16 * VW * c + VW * tx + x, o[r][c * VW + x]);
+        }
+    }
+    // the state behind the chunk
+    float u[NK][NV * VW] = {};
+#pragma unroll 2
+    for (int j = 0; j < kC; ++j) {
+      const float wj = j < n ? s.pw[back ? j + 1 : n - 1 - j] : 0.f;
+      float b[NV * VW];
+#pragma unroll
+      for (int c = 0; c < NV; ++c) {
+        float y[VW];
+        lds<VW>(&s.v[j][16 * VW * c + VW * tx], y);
+#pragma unroll
+        for (int x = 0; x < VW; ++x) b[c * VW + x] = wj * y[x];
+      }
+#pragma unroll
+      for (int a = 0; a < NK; ++a) {
+        const float kk = s.k[j][ty + 16 * a];
+#pragma unroll
+        for (int x = 0; x < NV * VW; ++x) u[a][x] = fmaf(kk, b[x], u[a][x]);
+      }
+    }
+    const float l0 = s.carry[0], l1 = s.carry[1];
+#pragma unroll
+    for (int a = 0; a < NK; ++a)
+#pragma unroll
+      for (int x = 0; x < NV * VW; ++x) X[a][x] = fmaf(X[a][x], l0, fmaf(X[a][x], l1, u[a][x]));
+    __syncthreads();
+  }
+
+  float *dst = SUMS ? p.ws + blockIdx.x * DD : (fin && op.s_out ? op.s_out + w.bh * DD : nullptr);
+  if (dst) {
+#pragma unroll
+    for (int a = 0; a < NK; ++a)
+#pragma unroll
+      for (int c = 0; c < NV; ++c)
+#pragma unroll
+        for (int e = 0; e < VW; ++e)
+          dst[(16 * VW * c + VW * tx + e) * D + ty + 16 * a] = X[a][c * VW + e];
+  }
+}
+
+// ws[seg] becomes the state in front of segment seg on the walk: it held what
+// the segment itself adds.
+__global__ void __launch_bounds__(256) decay_prefix_kernel(const DecayArgs p, int dd4) {
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long pair = i / dd4;
+  if (pair >= p.nops * p.BH) return;
+  const int e = (int)(i % dd4) * 4;
+  const DecayWork w = decay_work(p, pair * p.nseg);
+  const DecayOp &op = p.op[w.op];
+  const long long dd = (long long)dd4 * 4;
+  const float g = p.g[w.h];
+  const double full = decay_pow(g, p.seglen), tail = decay_pow(g, w.len - (long long)w.last_seg * p.seglen);
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  if (op.s_in) {
+    const float *src = op.s_in + w.bh * dd;
+    if (op.s_in_t) {
+      const int r = e / p.d, c = e % p.d;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[x] = src[(c + x) * p.d + r];
+    } else {
+      const float4 x = *reinterpret_cast<const float4 *>(src + e);
+      s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
+    }
+  }
+  float *ws = p.ws + pair * p.nseg * dd + e;
+  for (int n = 0; n <= w.last_seg; ++n) {
+    const int seg = op.back ? w.last_seg - n : n;
+    float4 *at = reinterpret_cast<float4 *>(ws + seg * dd);
+    const float4 u = n < w.last_seg ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+    *at = make_float4((float)s[0], (float)s[1], (float)s[2], (float)s[3]);
+    const double l = seg == w.last_seg ? tail : full;
+    s[0] = fma(s[0], l, (double)u.x);
+    s[1] = fma(s[1], l, (double)u.y);
+    s[2] = fma(s[2], l, (double)u.z);
+    s[3] = fma(s[3], l, (double)u.w);
+  }
+}
+
+template <typename TI, typename TO, int D, bool SUMS>
+cudaError_t launch_simt_t(const DecayArgs &a, cudaStream_t st) {
+  constexpr size_t smem = sizeof(SimtSmem<D>);
+  auto *kern = decay_simt_kernel<TI, TO, D, SUMS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(a.nops * a.BH * a.nseg), kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename TI, typename TO, bool SUMS>
+cudaError_t launch_simt_d(const DecayArgs &a, cudaStream_t st) {
+  switch (a.d) {
+    case 16: return launch_simt_t<TI, TO, 16, SUMS>(a, st);
+    case 32: return launch_simt_t<TI, TO, 32, SUMS>(a, st);
+    case 64: return launch_simt_t<TI, TO, 64, SUMS>(a, st);
+    case 128: return launch_simt_t<TI, TO, 128, SUMS>(a, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// ------------------------------------------------------------ single tokens
+// S' = l S + v k^T, o = S' q: bound by reading and writing the state once
+// (8 d^2 bytes per pair against 5 d^2 operations). A warp takes whole rows of
+// S, kLanes lanes to a row and 16 bytes per lane and load, so each load of a
+// warp covers full 128-byte lines; the row's product with q is summed over its
+// lanes by shuffles.
+constexpr int kStepThreads = 128;
+template <typename TI, typename TO, int D, int ITER>
+__global__ void __launch_bounds__(kStepThreads)
+    decay_step_kernel(const TI *Q, const TI *K, const TI *V, const float *g, const int32_t *active, const float *s_in,
+                      TO *O, float *s_out, long long rows, int H) {
+  constexpr int kLanes = D / 4 < 8 ? D / 4 : 8;  // lanes per row
+  constexpr int NV = D / (4 * kLanes);           // 16-byte vectors per lane
+  constexpr int RW = 32 / kLanes;                // rows per warp and iteration
+  const int lane = threadIdx.x & 31, sub = lane % kLanes;
+  const long long first = ((long long)blockIdx.x * (kStepThreads / 32) + (threadIdx.x >> 5)) * (RW * ITER) + lane / kLanes;
+  float4 s[ITER][NV];
+#pragma unroll
+  for (int it = 0; it < ITER; ++it) {
+    const long long row = first + it * RW;
+    if (row < rows) {
+#pragma unroll
+      for (int c = 0; c < NV; ++c) s[it][c] = *reinterpret_cast<const float4 *>(s_in + row * D + 4 * (sub + kLanes * c));
+    }
+  }
+#pragma unroll
+  for (int it = 0; it < ITER; ++it) {
+    const long long row = first + it * RW;
+    const bool there = row < rows;
+    const long long bh = (there ? row : 0) / D;
+    const bool on = there && (!active || active[bh / H] != 0);
+    float acc = 0.f;
+    if (on) {
+      const double l = exp((double)g[bh % H]);
+      const float l0 = (float)l, l1 = (float)(l - (double)l0);
+      const float v = to_f32(V[row]);
+#pragma unroll
+      for (int c = 0; c < NV; ++c) {
+        const long long at = bh * D + 4 * (sub + kLanes * c);
+        float *x = reinterpret_cast<float *>(&s[it][c]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = fmaf(x[e], l0, fmaf(x[e], l1, v * to_f32(K[at + e])));
+          acc = fmaf(x[e], to_f32(Q[at + e]), acc);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = kLanes / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+    if (there && (on || s_out != s_in)) {
+#pragma unroll
+      for (int c = 0; c < NV; ++c) *reinterpret_cast<float4 *>(s_out + row * D + 4 * (sub + kLanes * c)) = s[it][c];
+    }
+    if (on && sub == 0) store_val(O + row, acc);
+  }
+}
+
+template <typename TI, typename TO, int D>
+cudaError_t launch_step_t(const void *Q, const void *K, const void *V, const float *g, const int32_t *active,
+                          const float *s_in, void *O, float *s_out, long long BH, int H, cudaStream_t st) {
+  constexpr int kLanes = D / 4 < 8 ? D / 4 : 8;
+  constexpr int kRows = (32 / kLanes) * (kStepThreads / 32);  // rows per CTA and iteration
+  const long long rows = BH * D, grid = (rows + kRows - 1) / kRows;
+  decay_step_kernel<TI, TO, D, 1><<<(unsigned)grid, kStepThreads, 0, st>>>(
+      (const TI *)Q, (const TI *)K, (const TI *)V, g, active, s_in, (TO *)O, s_out, rows, H);
+  return cudaGetLastError();
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_step_d(const void *Q, const void *K, const void *V, const float *g, const int32_t *active,
+                          const float *s_in, void *O, float *s_out, long long BH, int H, int d, cudaStream_t st) {
+  switch (d) {
+    case 16: return launch_step_t<TI, TO, 16>(Q, K, V, g, active, s_in, O, s_out, BH, H, st);
+    case 32: return launch_step_t<TI, TO, 32>(Q, K, V, g, active, s_in, O, s_out, BH, H, st);
+    case 64: return launch_step_t<TI, TO, 64>(Q, K, V, g, active, s_in, O, s_out, BH, H, st);
+    case 128: return launch_step_t<TI, TO, 128>(Q, K, V, g, active, s_in, O, s_out, BH, H, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+DecaySplit decay_split(long long pairs, long long n) {
+  // Times in chunks of a walk: a wave of CTAs walks `len` chunks of its
+  // segment after a start of kStart chunks' time; more than one segment adds
+  // a pass for the states in front of the segments (half the traffic, no
+  // outputs) and their join.
+  constexpr long long kSms = 148, kStart = 4, kJoin = 6;
+  const long long chunks = (n + kDecayC - 1) / kDecayC;
+  long long best = 1, best_len = chunks > 0 ? chunks : 1, cost = -1;
+  for (long long want = 1; want <= chunks && want <= kSms; ++want) {
+    const long long len = (chunks + want - 1) / want, nseg = (chunks + len - 1) / len;
+    const long long waves = (pairs * nseg + kSms - 1) / kSms;
+    const long long c = 2 * waves * (len + kStart) + (nseg > 1 ? waves * (len + 2 * kStart) + 2 * kJoin : 0);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = nseg;
+      best_len = len;
+    }
+  }
+  return DecaySplit{(int)best, (int)(best_len * kDecayC)};
+}
+
+cudaError_t launch_decay_simt(const DecayArgs &a, int in_dtype, int out_dtype, bool sums, cudaStream_t st) {
+  if (in_dtype == VDN_F32) {
+    if (sums) return launch_simt_d<float, float, true>(a, st);
+    return out_dtype == VDN_F32 ? launch_simt_d<float, float, false>(a, st)
+                                : launch_simt_d<float, __nv_bfloat16, false>(a, st);
+  }
+  if (sums) return launch_simt_d<__nv_bfloat16, float, true>(a, st);
+  return out_dtype == VDN_F32 ? launch_simt_d<__nv_bfloat16, float, false>(a, st)
+                              : launch_simt_d<__nv_bfloat16, __nv_bfloat16, false>(a, st);
+}
+
+cudaError_t launch_decay_prefix(const DecayArgs &a, cudaStream_t st) {
+  const int dd4 = a.d * a.d / 4;
+  const long long n = a.nops * a.BH * dd4;
+  decay_prefix_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, dd4);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_decay_step(const void *Q, const void *K, const void *V, const float *g, const int32_t *active,
+                              const float *s_in, void *O, float *s_out, long long BH, int H, int d, int in_dtype,
+                              int out_dtype, cudaStream_t st) {
+  if (in_dtype == VDN_F32)
+    return out_dtype == VDN_F32
+               ? launch_step_d<float, float>(Q, K, V, g, active, s_in, O, s_out, BH, H, d, st)
+               : launch_step_d<float, __nv_bfloat16>(Q, K, V, g, active, s_in, O, s_out, BH, H, d, st);
+  return out_dtype == VDN_F32
+             ? launch_step_d<__nv_bfloat16, float>(Q, K, V, g, active, s_in, O, s_out, BH, H, d, st)
+             : launch_step_d<__nv_bfloat16, __nv_bfloat16>(Q, K, V, g, active, s_in, O, s_out, BH, H, d, st);
+}
+
+}  // namespace vdn

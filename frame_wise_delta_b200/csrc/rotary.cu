@@ -1,0 +1,178 @@
+// Rotary positions over several axes (time, height, width).
+//
+// The head's channels are cut into one section per axis (dim_t, dim_h, dim_w;
+// what is left over passes through). Pair i of an axis with n channels turns
+// by the angle pos * scale * theta^(-2 i / n):
+//   y_a = x_a cos - x_b sin,   y_b = x_a sin + x_b cos
+// with (a, b) = (2 i, 2 i + 1) of the section (interleaved) or (i, i + n / 2).
+//
+// Angles: pos * turns is formed in 64 bits and reduced to the nearest whole
+// turn there, so a stream's millionth frame keeps full float32 accuracy; the
+// sine and cosine of the remainder are taken in float32 (sincospif). A block
+// forms them once for its tokens, in shared memory, and applies them to every
+// head of every tensor.
+//
+// Bound by memory: each value is read and written once (2 d * size bytes per
+// row against 3 d operations), so a thread moves 16 bytes per access: whole
+// pairs when they are interleaved, the same stretch of both halves otherwise.
+// Sections that do not start on such a stretch take the widest one that divides
+// every section's half.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "decay.h"
+#include "internal.h"
+
+namespace vdn {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int BYTES> struct VecOf;
+template <> struct VecOf<2> { using T = uint16_t; };
+template <> struct VecOf<4> { using T = uint32_t; };
+template <> struct VecOf<8> { using T = uint2; };
+template <> struct VecOf<16> { using T = uint4; };
+
+template <typename T, int W>
+struct alignas(sizeof(T) * W) Pack {
+  T v[W];
+};
+
+template <typename T, int W>
+__device__ __forceinline__ Pack<T, W> load(const T *p) {
+  using V = typename VecOf<sizeof(T) * W>::T;
+  const V x = *reinterpret_cast<const V *>(p);
+  return *reinterpret_cast<const Pack<T, W> *>(&x);
+}
+template <typename T, int W>
+__device__ __forceinline__ void store(T *p, const Pack<T, W> &x) {
+  using V = typename VecOf<sizeof(T) * W>::T;
+  *reinterpret_cast<V *>(p) = *reinterpret_cast<const V *>(&x);
+}
+
+// One unit: PW pairs, either 2 PW neighbouring channels or PW channels of each
+// half. P: pairs per head (d / 2), the last `rest` of them pass through.
+template <typename T, int PW, bool INTER>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs p, int tokens, int slices) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const int P = p.d >> 1;
+  float2 *cs = reinterpret_cast<float2 *>(smem_raw);                     // [tokens][P]
+  double *turn = reinterpret_cast<double *>(cs + (size_t)tokens * P);    // [P]
+  const int b = blockIdx.z;
+  const long long n0 = (long long)blockIdx.x * tokens;
+  const int nt = (int)min((long long)tokens, p.N - n0);
+  const int rot = p.npairs[0] + p.npairs[1] + p.npairs[2];
+
+  for (int i = threadIdx.x; i < rot; i += kThreads) turn[i] = p.turn[i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < nt * rot; e += kThreads) {
+    const int t = e / rot, i = e - t * rot;
+    const int axis = i < p.npairs[0] ? 0 : i < p.npairs[0] + p.npairs[1] ? 1 : 2;
+    const long long n = n0 + t;
+    double at;
+    if (p.pos) {
+      at = (double)p.pos[((long long)b * p.N + n) * 3 + axis];
+    } else {
+      const long long f = n / p.U;
+      const int u = (int)(n - f * p.U);
+      at = axis == 0 ? (double)(p.frame0 + f) : axis == 1 ? (double)(u / p.gw) : (double)(u % p.gw);
+    }
+    const double a = at * turn[i];
+    float s, c;
+    sincospif(2.f * (float)(a - rint(a)), &s, &c);
+    cs[t * P + i] = make_float2(c, p.inverse ? -s : s);
+  }
+  __syncthreads();
+
+  // units of a row, then rows (tokens), then slices (tensor, head)
+  const int UR = P / PW;
+  const int per = nt * UR;
+  const int s0 = blockIdx.y * slices, s1 = min(s0 + slices, p.nio * p.H);
+  const int first1 = p.npairs[0], first2 = first1 + p.npairs[1];
+  for (int e = threadIdx.x; e < per; e += kThreads) {
+    const int t = e / UR, i = (e - t * UR) * PW;  // token, first pair
+    int lo, hi;                                   // channels of the first pair
+    if (INTER) {
+      lo = 2 * i;
+      hi = lo + PW;  // the second vector
+    } else {
+      const int f = i < first1 ? 0 : i < first2 ? first1 : i < rot ? first2 : rot;
+      const int n = i < first1 ? first1 : i < first2 ? p.npairs[1] : i < rot ? p.npairs[2] : P - rot;
+      lo = f + i;  // 2 f + (i - f)
+      hi = lo + n;
+    }
+    float2 w[PW];
+#pragma unroll
+    for (int x = 0; x < PW; ++x) w[x] = i + x < rot ? cs[t * P + i + x] : make_float2(1.f, 0.f);
+#pragma unroll 4
+    for (int sl = s0; sl < s1; ++sl) {
+      const int k = sl / p.H, h = sl - k * p.H;
+      const RotaryIo &io = p.io[k];
+      const T *x = (const T *)io.x + b * io.xs[0] + h * io.xs[1] + (n0 + t) * io.xs[2];
+      T *y = (T *)io.y + b * io.ys[0] + h * io.ys[1] + (n0 + t) * io.ys[2];
+      Pack<T, PW> A = load<T, PW>(x + lo), B = load<T, PW>(x + hi);
+      if (io.rotate) {
+#pragma unroll
+        for (int q = 0; q < PW; ++q) {
+          // pairs that pass through are copied, not turned by 0: 0 * inf is no number
+          if (i + q < rot) {
+            T &ra = INTER ? (2 * q < PW ? A.v[(2 * q) % PW] : B.v[(2 * q) % PW]) : A.v[q];
+            T &rb = INTER ? (2 * q + 1 < PW ? A.v[(2 * q + 1) % PW] : B.v[(2 * q + 1) % PW]) : B.v[q];
+            const float fa = to_f32(ra), fb = to_f32(rb);
+            store_val(&ra, fa * w[q].x - fb * w[q].y);
+            store_val(&rb, fa * w[q].y + fb * w[q].x);
+          }
+        }
+      }
+      store<T, PW>(y + lo, A);
+      store<T, PW>(y + hi, B);
+    }
+  }
+}
+
+template <typename T, int PW, bool INTER>
+cudaError_t launch_t(const RotaryArgs &a, cudaStream_t st) {
+  // tokens per block: enough for one unit per thread, at most 32 (the angles
+  // of a block are shared by all heads, so few tokens per block recompute
+  // nothing); the (tensor, head) slices are spread over blocks until the
+  // card has several blocks per SM
+  const int P = a.d / 2, UR = P / PW;
+  int tokens = (kThreads + UR - 1) / UR;
+  if (tokens < 8) tokens = 8;
+  if ((long long)tokens > a.N) tokens = (int)a.N;
+  const long long tiles = (a.N + tokens - 1) / tokens;
+  const int all = a.nio * a.H;
+  int slices = all;
+  while (slices > 1 && tiles * a.B * ((all + slices - 1) / slices) < 4 * 148) slices = (slices + 1) / 2;
+  const dim3 grid((unsigned)tiles, (unsigned)((all + slices - 1) / slices), (unsigned)a.B);
+  const size_t smem = (size_t)tokens * P * sizeof(float2) + (size_t)P * sizeof(double);
+  auto *kern = rotary_kernel<T, PW, INTER>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, smem, st>>>(a, tokens, slices);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_d(const RotaryArgs &a, cudaStream_t st) {
+  constexpr int W = 16 / sizeof(T);
+  if (a.interleaved) return launch_t<T, W, true>(a, st);
+  // the widest stretch that divides every section's start and half
+  int m = W;
+  const int rest = a.d / 2 - a.npairs[0] - a.npairs[1] - a.npairs[2];
+  for (const int n : {a.npairs[0], a.npairs[1], a.npairs[2], rest})
+    while (n % m) m /= 2;
+  if (m == 8) return launch_t<T, W, false>(a, st);
+  if (m == 4) return launch_t<T, 4, false>(a, st);
+  if (m == 2) return launch_t<T, 2, false>(a, st);
+  return launch_t<T, 1, false>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryArgs &a, int dtype, cudaStream_t st) {
+  return dtype == VDN_BF16 ? launch_d<__nv_bfloat16>(a, st) : launch_d<float>(a, st);
+}
+
+}  // namespace vdn

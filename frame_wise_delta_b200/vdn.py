@@ -92,6 +92,12 @@ _SIGS = {
     "vdn_selftest_wait": [_P, _P],
     "vdn_stream_segment": [_P] * 6 + [ctypes.c_longlong] + [_P] * 5 + [ctypes.c_size_t, _P, _P],
     "vdn_stream_segment_bridged": [_P] * 6 + [ctypes.c_longlong] + [_P] * 7 + [ctypes.c_size_t, _P, _P],
+    "vdn_rotary": [_P, _P, _P, ctypes.c_int32, _P],
+    "vdn_decay_attn_workspace_bytes": [_P],
+    "vdn_decay_attn": [_P] * 10 + [ctypes.c_size_t, _P, _P],
+    "vdn_decay_attn_backward_workspace_bytes": [_P],
+    "vdn_decay_attn_backward": [_P] * 14 + [ctypes.c_size_t, _P, _P],
+    "vdn_decay_step": [_P] * 10,
 }
 
 
@@ -108,7 +114,8 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
             fn.restype = ctypes.c_int
         for name in ("vdn_text_state_workspace_bytes", "vdn_forward_workspace_bytes",
-                     "vdn_stream_workspace_bytes"):
+                     "vdn_stream_workspace_bytes", "vdn_decay_attn_workspace_bytes",
+                     "vdn_decay_attn_backward_workspace_bytes"):
             fn = getattr(L, name)
             fn.argtypes = [_P]
             fn.restype = ctypes.c_size_t
@@ -291,6 +298,129 @@ def vdn_stream_segment_bridged(s, Q, K, V, beta, alpha, frame0, S_prev, S_in, al
                                             int(frame0), _ptr(S_prev), _ptr(S_in), _ptr(alpha_prev), _ptr(O),
                                             _ptr(F), _ptr(alpha_tail), _ptr(workspace), nbytes, _ptr(info),
                                             _stream(stream)))
+
+
+# ------------------------------------------------- token-level operators
+class vdn_rotary_args(ctypes.Structure):
+    _fields_ = [("grid_h", ctypes.c_int32), ("grid_w", ctypes.c_int32), ("dim_t", ctypes.c_int32),
+                ("dim_h", ctypes.c_int32), ("dim_w", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("frame0", ctypes.c_int64), ("theta", ctypes.c_double),
+                ("scale_t", ctypes.c_double), ("scale_h", ctypes.c_double), ("scale_w", ctypes.c_double),
+                ("pos", ctypes.c_void_p)]
+
+
+class vdn_rotary_io(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("x_stride", ctypes.c_int64 * 3),
+                ("y_stride", ctypes.c_int64 * 3), ("rotate", ctypes.c_int32)]
+
+
+def _here(*tensors):
+    """The token-level operators' tensors: on the current device (or None)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and (not t.is_cuda or t.get_device() != dev):
+            raise VdnError(VDN_ERR_INVALID, "tensor is not on the current CUDA device")
+
+
+def _typed(t, dtype, shape, name):
+    """t's pointer, or None for None; an int is a raw device pointer."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise VdnError(VDN_ERR_INVALID, f"{name} is {t.dtype} {tuple(t.shape)}, not {dtype} {shape}")
+    return _ptr(t)
+
+
+def rotary(dim_t, dim_h, dim_w, grid=(0, 0), interleaved=True, inverse=False, frame0=0, theta=10000.0,
+           scale=(1.0, 1.0, 1.0), pos=None):
+    """The arguments of vdn_rotary: channels of each axis, the frame's token
+    grid (rows, columns), or pos [B, T*U, 3] int32 with the position of every
+    token (keep the tensor alive while the result is in use)."""
+    if pos is not None and pos.dtype != torch.int32:
+        raise VdnError(VDN_ERR_INVALID, f"pos is {pos.dtype}, not torch.int32")
+    r = vdn_rotary_args(grid[0], grid[1], dim_t, dim_h, dim_w, int(bool(interleaved)), int(bool(inverse)), int(frame0),
+                        float(theta), float(scale[0]), float(scale[1]), float(scale[2]), _ptr(pos))
+    r.pos_tensor = pos
+    return r
+
+
+def _rows(t, s, name):
+    """(pointer, batch, head and token strides) of a [B, H, T, U, d] tensor."""
+    shape, st = t.shape, t.stride()
+    if tuple(shape) != (s.B, s.H, s.T, s.U, s.dk) or t.dtype != TORCH_DTYPE[s.in_dtype]:
+        raise VdnError(VDN_ERR_INVALID, f"{name} is {t.dtype} {tuple(shape)}, not the shape's")
+    if s.dk > 1 and st[4] != 1:
+        raise VdnError(VDN_ERR_INVALID, f"{name}'s channels are not contiguous")
+    if s.T > 1 and s.U > 1 and st[2] != st[3] * s.U:
+        raise VdnError(VDN_ERR_INVALID, f"{name}'s frames do not follow each other")
+    return t.data_ptr(), st[0], st[1], st[3] if s.U > 1 else st[2]
+
+
+def vdn_rotary(s, r, X, Y, rotate=None, stream=None):
+    """Rotates the tensors X into Y (lists of up to three [B, H, T, U, d]
+    tensors, token-major views included); rotate[i] = 0 copies X[i]."""
+    if len(X) != len(Y) or (rotate is not None and len(rotate) != len(X)):
+        raise VdnError(VDN_ERR_INVALID, "X, Y and rotate have different lengths")
+    pos = getattr(r, "pos_tensor", None)
+    _here(*X, *Y, pos)
+    if pos is not None and tuple(pos.shape) != (s.B, s.T * s.U, 3):
+        raise VdnError(VDN_ERR_INVALID, f"pos is {tuple(pos.shape)}, not {(s.B, s.T * s.U, 3)}")
+    io = (vdn_rotary_io * max(1, len(X)))()
+    for i, (x, y) in enumerate(zip(X, Y)):
+        e = io[i]
+        e.x, *e.x_stride[:] = _rows(x, s, "X")
+        e.y, *e.y_stride[:] = _rows(y, s, "Y")
+        e.rotate = 1 if rotate is None else int(rotate[i])
+    _check(lib().vdn_rotary(_shp(s), ctypes.byref(r), ctypes.byref(io), len(X), _stream(stream)))
+
+
+def vdn_decay_attn_workspace_bytes(s) -> int:
+    return int(lib().vdn_decay_attn_workspace_bytes(_shp(s)))
+
+
+def vdn_decay_attn_backward_workspace_bytes(s) -> int:
+    return int(lib().vdn_decay_attn_backward_workspace_bytes(_shp(s)))
+
+
+def _bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def vdn_decay_attn(s, Q, K, V, log_decay, lens, S_in, O, S_out, workspace, info=None, stream=None):
+    """Linear attention with one decay per head over the T * U tokens (see vdn.h); lens, S_in, S_out may be None."""
+    _here(Q, K, V, log_decay, lens, S_in, O, S_out, workspace, info)
+    x, st = (s.B, s.H, s.T, s.U, s.dk), (s.B, s.H, s.dv, s.dk)
+    ti, to, f = TORCH_DTYPE[s.in_dtype], TORCH_DTYPE[s.out_dtype], torch.float32
+    _check(lib().vdn_decay_attn(
+        _shp(s), _typed(Q, ti, x, "Q"), _typed(K, ti, x, "K"), _typed(V, ti, x, "V"),
+        _typed(log_decay, f, (s.H,), "log_decay"), _typed(lens, torch.int32, (s.B,), "lens"), _typed(S_in, f, st, "S_in"),
+        _typed(O, to, x, "O"), _typed(S_out, f, st, "S_out"), _ptr(workspace), _bytes(workspace), _ptr(info),
+        _stream(stream)))
+
+
+def vdn_decay_attn_backward(s, Q, K, V, log_decay, lens, S_in, dO, dS_out, dQ, dK, dV, dS_in, workspace, info=None,
+                            stream=None):
+    """Gradients of vdn_decay_attn (see vdn.h); lens, S_in, dS_out, dS_in may be None."""
+    _here(Q, K, V, log_decay, lens, S_in, dO, dS_out, dQ, dK, dV, dS_in, workspace, info)
+    x, st = (s.B, s.H, s.T, s.U, s.dk), (s.B, s.H, s.dv, s.dk)
+    ti, f = TORCH_DTYPE[s.in_dtype], torch.float32
+    _check(lib().vdn_decay_attn_backward(
+        _shp(s), _typed(Q, ti, x, "Q"), _typed(K, ti, x, "K"), _typed(V, ti, x, "V"),
+        _typed(log_decay, f, (s.H,), "log_decay"), _typed(lens, torch.int32, (s.B,), "lens"), _typed(S_in, f, st, "S_in"),
+        _typed(dO, ti, x, "dO"), _typed(dS_out, f, st, "dS_out"), _typed(dQ, ti, x, "dQ"), _typed(dK, ti, x, "dK"),
+        _typed(dV, ti, x, "dV"), _typed(dS_in, f, st, "dS_in"), _ptr(workspace), _bytes(workspace), _ptr(info),
+        _stream(stream)))
+
+
+def vdn_decay_step(s, Q, K, V, log_decay, active, S_in, O, S_out, stream=None):
+    """One token per sequence of vdn_decay_attn (see vdn.h); Q, K, V, O [B, H, d], S_out may be S_in."""
+    _here(Q, K, V, log_decay, active, S_in, O, S_out)
+    x, st = (s.B, s.H, s.dk), (s.B, s.H, s.dv, s.dk)
+    ti, to, f = TORCH_DTYPE[s.in_dtype], TORCH_DTYPE[s.out_dtype], torch.float32
+    _check(lib().vdn_decay_step(
+        _shp(s), _typed(Q, ti, x, "Q"), _typed(K, ti, x, "K"), _typed(V, ti, x, "V"),
+        _typed(log_decay, f, (s.H,), "log_decay"), _typed(active, torch.int32, (s.B,), "active"),
+        _typed(S_in, f, st, "S_in"), _typed(O, to, x, "O"), _typed(S_out, f, st, "S_out"), _stream(stream)))
 
 
 def vdn_selftest_wait(info, stream=None):

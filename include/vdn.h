@@ -409,6 +409,126 @@ vdn_status vdn_stream_segment_bridged(const vdn_shape *s, const void *Q,
                                       int32_t *info, vdn_stream_t stream);
 
 /*
+ * Token-level operators. They take the same vdn_shape; a (batch, head) pair's
+ * token sequence is its T * U tokens in order (T = 1, U = n for plain
+ * sequences), n_text, chunk, anchors, beta_per_token and decay_bridge are
+ * checked but not used. They work on the current device: every pointer is
+ * memory of that device.
+ */
+
+/*
+ * Rotary positions over (time, height, width). Paper: "Method steps" step (1)
+ * (the softmax branch's Q and K carry rotary positions).
+ * Channels 0 .. dim_t - 1 of a head turn with the token's frame, the next
+ * dim_h with its row, the next dim_w with its column; the rest pass through
+ * unchanged. Pair i of an axis with n channels turns by
+ *   pos * scale * theta^(-2 i / n):
+ *   y_a = x_a cos - x_b sin,  y_b = x_a sin + x_b cos,
+ * (a, b) = channels (2 i, 2 i + 1) of the axis' section (interleaved = 1) or
+ * (i, i + n / 2) (interleaved = 0). inverse = 1 turns the other way: the
+ * transposed rotation, which is the gradient's. Angles are reduced in float64
+ * and the products taken in float32, so far positions keep their accuracy.
+ */
+typedef struct {
+  int32_t grid_h, grid_w;       /* token u of a frame is row u / grid_w, column
+                                   u % grid_w; grid_h * grid_w = U (not used
+                                   with pos) */
+  int32_t dim_t, dim_h, dim_w;  /* channels of each axis: even, >= 0, their sum
+                                   at most dk */
+  int32_t interleaved, inverse; /* 0 or 1 */
+  int64_t frame0;               /* position of frame 0 (a stream's running frame
+                                   count), within +-2^52 */
+  double theta;                 /* > 0 */
+  double scale_t, scale_h, scale_w; /* positions are multiplied by these */
+  const int32_t *pos;           /* device [B, T*U, 3] (t, h, w) of every token,
+                                   or NULL: frame0 + t and the grid */
+} vdn_rotary_args;
+
+/*
+ * One tensor of a vdn_rotary call, [B, H, T*U, dk] in in_dtype on both sides,
+ * channels contiguous, the other axes by strides in elements (batch, head,
+ * token): so Q, K and V can be read where a projection left them, token-major,
+ * and written in the [B, H, T, U, d] layout of the other calls. Strides are
+ * multiples of 16 bytes; x's may be 0 (a broadcast axis), y's rows may not
+ * overlap. y may be x with the same strides; no other overlap is allowed.
+ */
+typedef struct {
+  const void *x;
+  void *y;
+  int64_t x_stride[3], y_stride[3];
+  int32_t rotate; /* 1: turned; 0: copied (V on its way to the other layout) */
+} vdn_rotary_io;
+
+/*
+ * Rotates (or copies) n_io tensors, 1 to 3, in one launch.
+ * Errors: VDN_ERR_INVALID for axes that do not fit, a grid that is not U
+ * tokens, strides as above, a non-positive or non-finite theta, a non-finite
+ * scale; VDN_ERR_UNSUPPORTED for B > 65535 or n_io * H > 65535.
+ */
+vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_rotary_io *io,
+                      int32_t n_io, vdn_stream_t stream);
+
+/*
+ * Decay attention: linear attention over the token sequence with one decay per
+ * head, the additive memory that the frame-wise delta rule is set against
+ * (paper: "Core method", the memory S maps a key to a value; here a token's
+ * write is not corrected by what the memory holds). With l = exp(log_decay[h]),
+ *   S_i = l S_{i-1} + v_i k_i^T,   o_i = S_i q_i,   i = 0 .. n - 1,
+ * S_{-1} = S_in. Computed in chunks of 64 tokens (the causal products inside a
+ * chunk, the state in front of it for the rest), long sequences in segments.
+ * In : Q, K, V [B,H,T,U,d] (in_dtype); log_decay [H] float32, <= 0 (0 keeps
+ *      everything, -inf only the token itself; positive or NaN values give
+ *      unspecified results); lens [B] int32 or NULL: tokens of each sequence,
+ *      clamped to [0, T*U]. What lies behind a sequence's last token is not
+ *      used, whatever it holds, and O is left as it was there. S_in
+ *      [B,H,dv,dk] float32 or NULL (zero).
+ * Out: O [B,H,T,U,dv] (out_dtype); S_out [B,H,dv,dk] float32 or NULL: the state
+ *      behind the last token (S_in for an empty sequence); may be S_in.
+ * Values have to be finite: one that is not spoils its sequence's outputs from
+ * the start of its 64-token chunk on.
+ * info: optional, as for vdn_frame_grams.
+ * workspace: at least vdn_decay_attn_workspace_bytes(s) bytes (0 for short
+ * sequences: it may then be NULL), 256-byte aligned.
+ * Precision: float32 sums and state.
+ */
+size_t vdn_decay_attn_workspace_bytes(const vdn_shape *s);
+vdn_status vdn_decay_attn(const vdn_shape *s, const void *Q, const void *K, const void *V,
+                          const float *log_decay, const int32_t *lens, const float *S_in, void *O,
+                          float *S_out, void *workspace, size_t workspace_bytes, int32_t *info,
+                          vdn_stream_t stream);
+
+/*
+ * Gradients of vdn_decay_attn for dO (of O) and dS_out (of S_out, NULL: zero):
+ *   dq_i = S_i^T do_i,  Z_i = l Z_{i+1} + do_i q_i^T (Z_{n-1} = dS_out + do q^T),
+ *   dk_i = Z_i^T v_i,  dv_i = Z_i k_i,  dS_in = l Z_0   (dS_out for n = 0),
+ * log_decay being a constant. The states are recomputed, nothing of the
+ * forward pass is needed but its inputs. in_dtype has to be out_dtype
+ * (VDN_ERR_UNSUPPORTED).
+ * In : as for vdn_decay_attn, dO [B,H,T,U,dv] (its rows behind a sequence's end
+ *      are not used), dS_out [B,H,dv,dk] float32 or NULL.
+ * Out: dQ, dK, dV [B,H,T,U,d] (in_dtype; left as they were behind a sequence's
+ *      end), dS_in [B,H,dv,dk] float32 or NULL. No output may be an input.
+ */
+size_t vdn_decay_attn_backward_workspace_bytes(const vdn_shape *s);
+vdn_status vdn_decay_attn_backward(const vdn_shape *s, const void *Q, const void *K, const void *V,
+                                   const float *log_decay, const int32_t *lens, const float *S_in,
+                                   const void *dO, const float *dS_out, void *dQ, void *dK,
+                                   void *dV, float *dS_in, void *workspace, size_t workspace_bytes,
+                                   int32_t *info, vdn_stream_t stream);
+
+/*
+ * One token per (batch, head) of decay attention (T = U = 1): the recurrence
+ * itself, with the state read and written once.
+ * In : Q, K, V [B,H,d] (in_dtype); log_decay [H] as above; active [B] int32 or
+ *      NULL: a sequence whose word is 0 keeps its state and its row of O;
+ *      S_in [B,H,dv,dk] float32.
+ * Out: O [B,H,dv] (out_dtype), S_out [B,H,dv,dk] float32; may be S_in.
+ */
+vdn_status vdn_decay_step(const vdn_shape *s, const void *Q, const void *K, const void *V,
+                          const float *log_decay, const int32_t *active, const float *S_in, void *O,
+                          float *S_out, vdn_stream_t stream);
+
+/*
  * Self-test of the bounded pipeline waits that every tensor-core kernel uses:
  * launches one CTA whose threads wait, through the same bounded wait, on a
  * barrier that nothing arrives at. The wait gives up after its limit (1.5 s

@@ -1,0 +1,470 @@
+"""GPU parity of the token-level operators (rotary positions, decay attention,
+its gradients, single tokens) with their float64 definitions, their edges
+(ragged and empty sequences, poisoned padding, heads that forget nothing or
+everything, segments, far positions, strided tensors) and a run of them
+together.
+
+Tolerances. Half a step is u = 2^-8 (bf16) or 2^-24 (float32) of a value. A
+bf16 output is rounded once (u |o|); the decayed scores are rounded to bf16 too
+(u M_i, M_i = sum_j l^|i-j| |q_i . k_j| |v_j|); the state enters the products as
+two bf16 parts and everything else is float32, with rounded sums of at most
+d + n + 64 terms: below 2^-13 of A_i (M_i with |q|.|k|, and |S| |q|) for the
+sizes here. A float32 output is off by 2^-24 (d + 128 + n / 64) A_i at most.
+States: in float32 each product is off by 2^-23 at most and a sum of t rounded
+additions of random sign by sqrt(t) half steps, t < 600: 2e-6 of the norm."""
+import numpy as np
+import pytest
+import torch
+
+from frame_wise_delta_b200 import vdn
+from oracle import token_ops as tok
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _build():
+    from frame_wise_delta_b200 import build
+    build.build()
+    assert torch.cuda.is_available()
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _inputs(seed, B, H, T, U, d, dt, names="qkv", g=None):
+    r = np.random.default_rng(seed)
+    x = {}
+    for n in names:
+        a = r.standard_normal((B, H, T, U, d))
+        if n == "k":
+            a /= np.linalg.norm(a, axis=-1, keepdims=True)
+        x[n] = torch.from_numpy(a).to("cuda").to(DT[dt])
+    if g is None:
+        g = -np.exp(r.uniform(np.log(1e-4), np.log(0.7), H))
+        g[0] = 0.0
+    x["g"] = torch.tensor(np.asarray(g, np.float32), device="cuda")
+    x["s"] = torch.from_numpy(r.standard_normal((B, H, d, d)).astype(np.float32) * 0.5).cuda()
+    x["z"] = torch.from_numpy(r.standard_normal((B, H, d, d)).astype(np.float32) * 0.5).cuda()
+    return x
+
+
+def _flat(t):
+    return _np(t).reshape(t.shape[0], t.shape[1], -1, t.shape[-1])
+
+
+def _near(got, ref, m, a, dt, n, d):
+    """|got - ref| within the bound, element by element, on the rows that ref has."""
+    rows = np.isfinite(ref)
+    if dt == "bf16":
+        tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -8 * 1.01 * m + 2.0 ** -13 * a
+    else:
+        tol = 2.0 ** -24 * (d + 128 + n / 64) * a + 2.0 ** -24 * np.abs(ref)
+    off = np.abs(got - ref)[rows] - tol[rows]
+    assert np.isfinite(got[rows]).all()
+    assert off.size == 0 or off.max() <= 0, float(off.max())
+
+
+def _state_near(got, ref):
+    assert np.linalg.norm(got - ref) <= 2e-6 * np.linalg.norm(ref)
+
+
+def _poison(x, lens, names):
+    """NaN and infinities behind each sequence's end."""
+    for b, n in enumerate(lens):
+        for k, name in enumerate(names):
+            t = x[name].view(x[name].shape[0], x[name].shape[1], -1, x[name].shape[-1])
+            t[b, :, n:] = [float("nan"), float("inf"), float("-inf"), 3e38][(b + k) % 4]
+
+
+MARK = 7.0
+
+
+def _attn(s, x, lens=None, s_in=True, s_out=None, stream=None):
+    o = torch.full((s.B, s.H, s.T, s.U, s.dk), MARK, dtype=vdn.TORCH_DTYPE[s.out_dtype], device="cuda")
+    if s_out is None:
+        s_out = torch.full_like(x["s"], float("nan"))
+    ws = vdn.workspace(vdn.vdn_decay_attn_workspace_bytes(s))
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lt = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    vdn.vdn_decay_attn(s, x["q"], x["k"], x["v"], x["g"], lt, x["s"] if s_in else None, o, s_out, ws, info, stream)
+    torch.cuda.synchronize()
+    assert int(info.item()) == 0
+    return o, s_out
+
+
+CASES = [
+    # B, H, T, U, d, in, out, lens, state
+    (1, 1, 1, 1, 16, "f32", "f32", None, True),
+    (2, 3, 1, 1, 128, "bf16", "bf16", None, True),
+    (1, 2, 3, 21, 32, "bf16", "bf16", None, False),
+    (2, 2, 1, 64, 64, "bf16", "bf16", None, True),
+    (1, 3, 1, 65, 128, "bf16", "bf16", None, True),
+    (2, 2, 5, 26, 128, "bf16", "bf16", None, False),
+    (1, 2, 1, 257, 16, "bf16", "bf16", None, True),
+    (5, 2, 1, 200, 128, "bf16", "bf16", [200, 0, 1, 64, 129], True),
+    (5, 2, 1, 200, 64, "bf16", "bf16", [63, 0, 200, 65, 1], True),
+    (4, 2, 1, 150, 32, "bf16", "bf16", [150, 149, 0, 128], False),
+    (4, 2, 2, 75, 64, "f32", "f32", [150, 0, 7, 64], True),
+    (2, 2, 1, 130, 128, "f32", "f32", None, True),
+    (2, 2, 1, 100, 32, "bf16", "f32", [100, 33], True),
+    (2, 2, 1, 100, 16, "f32", "bf16", None, False),
+    (1, 1, 1, 2500, 128, "bf16", "bf16", None, True),   # several segments
+    (2, 1, 1, 2500, 64, "bf16", "bf16", [2500, 1300], True),
+    (3, 1, 1, 2500, 32, "f32", "f32", [2500, 64, 0], True),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_attention(case):
+    B, H, T, U, d, di, do, lens, state = case
+    x = _inputs(11 + d + U, B, H, T, U, d, di)
+    if lens:
+        _poison(x, lens, "qkv")
+    s = vdn.make_shape(B, H, T, U, d, 0, in_dtype=di, out_dtype=do)
+    o, s1 = _attn(s, x, lens, state)
+    q, k, v = (_flat(x[n]) for n in "qkv")
+    s0 = _np(x["s"]) if state else None
+    ref, ref_s = tok.decay_attn(q, k, v, _np(x["g"]), lens, s0)
+    keep = np.isfinite(ref)
+    q, k, v = (np.where(keep, y, 0.0) for y in (q, k, v))
+    m, a = tok.decay_scale(q, k, v, _np(x["g"]), s0)
+    _near(_flat(o), ref, m, a, "f32" if do == "f32" else "bf16", T * U, d)
+    _state_near(_np(s1), ref_s)
+    # rows behind the end are left as they were
+    assert (_flat(o)[~keep] == MARK).all()
+    # and the call gives the same bits again
+    o2, s2 = _attn(s, x, lens, state)
+    assert torch.equal(o, o2) and torch.equal(s1, s2)
+
+
+@pytest.mark.parametrize("d,di", [(128, "bf16"), (64, "bf16"), (32, "f32")])
+def test_attention_decays(d, di):
+    """Heads that forget nothing, everything, and nearly either."""
+    g = [0.0, float("-inf"), -1e-7, -0.3, -0.65, -0.9, -5.0, -80.0]
+    x = _inputs(5, 1, len(g), 1, 300, d, di, g=g)
+    s = vdn.make_shape(1, len(g), 1, 300, d, 0, in_dtype=di)
+    o, s1 = _attn(s, x)
+    q, k, v = (_flat(x[n]) for n in "qkv")
+    ref, ref_s = tok.decay_attn(q, k, v, np.array(g), None, _np(x["s"]))
+    m, a = tok.decay_scale(q, k, v, np.array(g), _np(x["s"]))
+    _near(_flat(o), ref, m, a, di, 300, d)
+    for h in range(len(g)):
+        _state_near(_np(s1)[:, h], ref_s[:, h])
+
+
+@pytest.mark.parametrize("di", ["bf16", "f32"])
+def test_state_in_place_and_empty(di):
+    x = _inputs(6, 2, 2, 1, 70, 64, di)
+    s = vdn.make_shape(2, 2, 1, 70, 64, 0, in_dtype=di)
+    o, s1 = _attn(s, x)
+    st = x["s"].clone()
+    o2, _ = _attn(s, {**x, "s": st}, s_out=st)
+    assert torch.equal(o, o2) and torch.equal(st, s1)
+    s0 = vdn.make_shape(2, 2, 0, 70, 64, 0, in_dtype=di)
+    e = {**x, **{n: x[n][:, :, :0] for n in "qkv"}}
+    _, s2 = _attn(s0, e)
+    assert torch.equal(s2, x["s"])
+    _, s2 = _attn(s0, e, s_in=False)
+    assert (s2 == 0).all()
+
+
+def test_attention_without_final_state_or_info():
+    x = _inputs(7, 1, 2, 1, 90, 128, "bf16")
+    s = vdn.make_shape(1, 2, 1, 90, 128, 0)
+    o = torch.empty_like(x["q"])
+    vdn.vdn_decay_attn(s, x["q"], x["k"], x["v"], x["g"], None, x["s"], o, None, None)
+    torch.cuda.synchronize()
+    assert torch.equal(o, _attn(s, x)[0])
+
+
+BACK = [
+    (1, 2, 1, 1, 16, "f32", None, True),
+    (2, 2, 1, 1, 128, "bf16", None, True),
+    (1, 3, 3, 31, 128, "bf16", None, True),
+    (2, 2, 1, 64, 64, "bf16", None, False),
+    (5, 2, 1, 200, 128, "bf16", [200, 0, 1, 64, 129], True),
+    (4, 2, 1, 150, 32, "bf16", [150, 149, 0, 128], False),
+    (4, 2, 2, 75, 64, "f32", [150, 0, 7, 64], True),
+    (2, 2, 1, 130, 128, "f32", None, True),
+    (1, 1, 1, 2500, 128, "bf16", None, True),
+    (2, 1, 1, 2500, 64, "bf16", [2500, 1300], True),
+    (3, 1, 1, 2500, 32, "f32", [2500, 64, 0], True),
+]
+
+
+def _backward(s, x, lens=None, state=True):
+    lt = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = [torch.full_like(x["q"], MARK) for _ in range(3)]
+    ds = torch.full_like(x["s"], float("nan"))
+    ws = vdn.workspace(vdn.vdn_decay_attn_backward_workspace_bytes(s))
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+    vdn.vdn_decay_attn_backward(s, x["q"], x["k"], x["v"], x["g"], lt, x["s"] if state else None, x["o"],
+                                x["z"] if state else None, *out, ds, ws, info)
+    torch.cuda.synchronize()
+    assert int(info.item()) == 0
+    return out, ds
+
+
+@pytest.mark.parametrize("case", BACK, ids=str)
+def test_backward(case):
+    B, H, T, U, d, dt, lens, state = case
+    x = _inputs(31 + d + U, B, H, T, U, d, dt, names="qkvo")
+    if lens:
+        _poison(x, lens, "qkvo")
+    s = vdn.make_shape(B, H, T, U, d, 0, in_dtype=dt)
+    out, ds = _backward(s, x, lens, state)
+    q, k, v, do = (_flat(x[n]) for n in "qkvo")
+    s0, z = (_np(x["s"]), _np(x["z"])) if state else (None, None)
+    g = _np(x["g"])
+    *refs, ref_s = tok.decay_attn_backward(q, k, v, g, do, lens, s0, z)
+    keep = np.isfinite(refs[0])
+    q, k, v, do = (np.where(keep, y, 0.0) for y in (q, k, v, do))
+    tr = lambda t: None if t is None else np.swapaxes(t, -1, -2)  # noqa: E731
+    scales = [tok.decay_scale(do, v, k, g, tr(s0)), tok.decay_scale(v, do, q, g, tr(z), back=True),
+              tok.decay_scale(k, q, do, g, z, back=True)]
+    for got, ref, (m, a) in zip(out, refs, scales):
+        _near(_flat(got), ref, m, a, dt, T * U, d)
+        assert (_flat(got)[~keep] == MARK).all()
+    _state_near(_np(ds), ref_s)
+
+
+def test_backward_decays():
+    g = [0.0, float("-inf"), -1e-7, -0.3, -0.65, -0.9, -5.0, -80.0]
+    x = _inputs(8, 1, len(g), 1, 300, 128, "bf16", names="qkvo", g=g)
+    s = vdn.make_shape(1, len(g), 1, 300, 128, 0)
+    out, ds = _backward(s, x)
+    q, k, v, do = (_flat(x[n]) for n in "qkvo")
+    s0, z = _np(x["s"]), _np(x["z"])
+    *refs, ref_s = tok.decay_attn_backward(q, k, v, np.array(g), do, None, s0, z)
+    tr = lambda t: np.swapaxes(t, -1, -2)  # noqa: E731
+    scales = [tok.decay_scale(do, v, k, np.array(g), tr(s0)), tok.decay_scale(v, do, q, np.array(g), tr(z), back=True),
+              tok.decay_scale(k, q, do, np.array(g), z, back=True)]
+    for got, ref, (m, a) in zip(out, refs, scales):
+        _near(_flat(got), ref, m, a, "bf16", 300, 128)
+    for h in range(len(g)):
+        assert np.linalg.norm(_np(ds)[:, h] - ref_s[:, h]) <= 2e-6 * np.linalg.norm(ref_s[:, h]) + 1e-30
+
+
+def test_backward_is_the_difference():
+    """The gradients against central differences of the float32 forward pass,
+    summed in float64: the loss is linear in each argument, so a difference is
+    off by the rounding of the outputs alone (2^-24 each, over the step)."""
+    x = _inputs(9, 1, 2, 1, 80, 32, "f32", names="qkvo")
+    s = vdn.make_shape(1, 2, 1, 80, 32, 0, in_dtype="f32")
+    out, ds = _backward(s, x)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def loss(y):
+        o, s1 = _attn(s, y)
+        return float((o.double() * x["o"].double()).sum() + (s1.double() * x["z"].double()).sum())
+
+    mag = float((_attn(s, x)[0].double() * x["o"].double()).abs().sum() + (_attn(s, x)[1].double() * x["z"].double()).abs().sum())
+    for name, grad in zip("qkvs", [*out, ds]):
+        e = torch.randn(x[name].shape, generator=gen, device="cuda")
+        h = 0.25
+        diff = (loss({**x, name: x[name] + h * e}) - loss({**x, name: x[name] - h * e})) / (2 * h)
+        # both losses hold sums of about `mag` whose terms carry 2^-20 each at most
+        assert abs(diff - float((grad.double() * e.double()).sum())) <= 2.0 ** -20 * mag / h
+
+
+STEP = [(1, 1, 16, "f32", "f32", None), (3, 5, 32, "bf16", "bf16", [1, 0, 1]), (2, 3, 64, "bf16", "f32", None),
+        (4, 24, 128, "bf16", "bf16", [0, 1, 5, 0]), (2, 2, 128, "f32", "f32", None), (2, 3, 16, "f32", "bf16", [0, -1])]
+
+
+@pytest.mark.parametrize("case", STEP, ids=str)
+@pytest.mark.parametrize("in_place", [False, True])
+def test_step(case, in_place):
+    B, H, d, di, do, active = case
+    g = [[0.0, float("-inf"), -0.01, -2.0][h % 4] for h in range(H)]
+    x = _inputs(40 + d, B, H, 1, 1, d, di, g=g)
+    s = vdn.make_shape(B, H, 1, 1, d, 0, in_dtype=di, out_dtype=do)
+    q, k, v = (x[n].view(B, H, d) for n in "qkv")
+    lens = None if active is None else [int(a != 0) for a in active]
+    if lens:
+        for t in (q, k, v):
+            t[[b for b in range(B) if not lens[b]]] = float("nan")
+    o = torch.full((B, H, d), MARK, dtype=DT[do], device="cuda")
+    st = x["s"].clone()
+    s1 = st if in_place else torch.full_like(st, float("nan"))
+    vdn.vdn_decay_step(s, q, k, v, x["g"], None if active is None else torch.tensor(active, dtype=torch.int32, device="cuda"),
+                       st, o, s1)
+    torch.cuda.synchronize()
+    fq, fk, fv = (_flat(x[n]) for n in "qkv")
+    ref, ref_s = tok.decay_attn(fq, fk, fv, np.array(g), lens, _np(x["s"]))
+    keep = np.isfinite(ref)
+    fq, fk, fv = (np.where(keep, y, 0.0) for y in (fq, fk, fv))
+    _, a = tok.decay_scale(fq, fk, fv, np.array(g), _np(x["s"]))
+    got = _np(o)[:, :, None]
+    u = 2.0 ** -8 if do == "bf16" else 2.0 ** -24
+    tol = u * np.abs(ref) + 2.0 ** -24 * (d + 4) * a
+    assert (np.abs(got - ref)[keep] <= tol[keep]).all()
+    assert (got[~keep] == MARK).all()
+    _state_near(_np(s1), ref_s)
+    if lens:
+        off = [b for b in range(B) if not lens[b]]
+        assert torch.equal(s1[off], x["s"][off])
+
+
+ROT = [
+    # B, H, T, gh, gw, d, dtype, dims, interleaved, inverse, frame0, scale
+    (1, 1, 1, 1, 1, 16, "f32", (16, 0, 0), True, False, 0, 1.0),
+    (2, 3, 3, 5, 7, 128, "bf16", (44, 42, 42), True, False, 0, 1.0),
+    (2, 3, 3, 5, 7, 128, "bf16", (44, 42, 42), False, False, 3, 0.5),
+    (1, 2, 2, 4, 9, 128, "bf16", (16, 56, 56), False, True, 0, 1.0),
+    (1, 2, 2, 4, 9, 64, "f32", (20, 20, 20), False, False, 999999937, 1.25),
+    (2, 1, 4, 3, 3, 64, "f32", (0, 30, 34), True, True, 0, 1.0),
+    (1, 5, 2, 3, 5, 32, "bf16", (0, 0, 0), True, False, 0, 1.0),
+    (1, 2, 70, 1, 2, 32, "bf16", (8, 4, 4), False, False, 1 << 40, 0.25),
+    (3, 2, 1, 1, 700, 16, "f32", (2, 2, 10), False, False, 0, 1.0),
+]
+
+
+@pytest.mark.parametrize("case", ROT, ids=str)
+@pytest.mark.parametrize("layout", ["head", "token", "given"])
+def test_rotary(case, layout):
+    B, H, T, gh, gw, d, dt, dims, inter, inv, frame0, scale = case
+    U, n = gh * gw, T * gh * gw
+    r = np.random.default_rng(60 + d + n)
+    if layout == "token":
+        qkv = torch.from_numpy(r.standard_normal((B, n, 3, H, d))).cuda().to(DT[dt])
+        xs = [qkv[:, :, i].permute(0, 2, 1, 3).unflatten(2, (T, U)) for i in range(3)]
+    else:
+        xs = [torch.from_numpy(r.standard_normal((B, H, T, U, d))).cuda().to(DT[dt]) for _ in range(2)]
+    rest = sum(dims)
+    if rest < d:
+        xs[0][..., rest] = float("inf")  # passes through, and spoils nobody
+        xs[0][..., d - 1] = float("nan")
+    pos, pos_t = tok.grid_positions(T, gh, gw, frame0), None
+    if layout == "given":
+        pos = r.integers(-5, 2000000, (B, n, 3))
+        pos_t = torch.from_numpy(pos.astype(np.int32)).cuda()
+    s = vdn.make_shape(B, H, T, U, d, 0, in_dtype=dt)
+    rot = vdn.rotary(*dims, grid=(gh, gw), interleaved=inter, inverse=inv, frame0=frame0, theta=1000.0, scale=(scale, 1.0, scale),
+                     pos=pos_t)
+    ys = [torch.full((B, H, T, U, d), MARK, dtype=DT[dt], device="cuda") for _ in xs]
+    turned = [1, 1, 0][:len(xs)]
+    vdn.vdn_rotary(s, rot, xs, ys, turned)
+    torch.cuda.synchronize()
+    u = 2.0 ** -8 if dt == "bf16" else 2.0 ** -24
+    for x, y, t in zip(xs, ys, turned):
+        if not t:
+            assert torch.equal(x, y)
+            continue
+        assert torch.equal(x[..., rest:].nan_to_num(1.0, 2.0), y[..., rest:].nan_to_num(1.0, 2.0))
+        f, got = _flat(x)[..., :rest], _flat(y)[..., :rest]
+        ref = tok.rotary(f, pos, dims, 1000.0, (scale, 1.0, scale), inter, inv)
+        # the remainder of a turn, its sine and cosine (2 steps each) and the two
+        # products in float32: under 16 half steps of the largest value, then the
+        # output's rounding; beyond 2^40 turns the product in float64 itself is 2^-12 turns off
+        tol = u * np.abs(ref) + (2.0 ** -20 + (0.01 if frame0 > 1 << 30 else 0)) * np.abs(f).max(initial=0)
+        assert (np.abs(got - ref) <= tol).all()
+    # in place
+    if layout != "token":
+        z = [x.clone() for x in xs]
+        vdn.vdn_rotary(s, rot, z, z, turned)
+        assert all(torch.equal(a.nan_to_num(1.0, 2.0), b.nan_to_num(1.0, 2.0)) for a, b in zip(z, ys))
+
+
+def test_rotary_inverse_undoes():
+    x = torch.randn(2, 3, 4, 35, 64, device="cuda")
+    s = vdn.make_shape(2, 3, 4, 35, 64, 0, in_dtype="f32")
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    for inter in (True, False):
+        vdn.vdn_rotary(s, vdn.rotary(20, 22, 22, grid=(5, 7), interleaved=inter, frame0=123456), [x], [y])
+        vdn.vdn_rotary(s, vdn.rotary(20, 22, 22, grid=(5, 7), interleaved=inter, frame0=123456, inverse=True), [y], [z])
+        # two rotations, each off by 16 half steps of the largest value at most
+        assert float((x - z).abs().max()) <= 32 * 2.0 ** -24 * float(x.abs().max())
+
+
+def _serve(prompt, steps, B, H, d, dt):
+    """A prompt's tokens, then single tokens, from a token-major projection."""
+    n = prompt + steps
+    r = np.random.default_rng(77)
+    qkv = torch.from_numpy(r.standard_normal((B, n, 3, H, d)) * 0.3).cuda().to(DT[dt])
+    g = torch.tensor([0.0, -0.02, -0.5][:H], device="cuda")
+    dims = (d // 2, d // 4, d // 4)
+
+    def rotated(a, b):
+        s = vdn.make_shape(B, H, b - a, 1, d, 0, in_dtype=dt)
+        xs = [qkv[:, a:b, i].permute(0, 2, 1, 3).unflatten(2, (b - a, 1)) for i in range(3)]
+        ys = [torch.empty((B, H, b - a, 1, d), dtype=DT[dt], device="cuda") for _ in xs]
+        vdn.vdn_rotary(s, vdn.rotary(*dims, grid=(1, 1), frame0=a), xs, ys, [1, 1, 0])
+        return s, ys
+
+    def attend(a, b, state):
+        s, (q, k, v) = rotated(a, b)
+        o, st = torch.empty_like(q), torch.empty((B, H, d, d), device="cuda")
+        ws = vdn.workspace(vdn.vdn_decay_attn_workspace_bytes(s))
+        vdn.vdn_decay_attn(s, q, k, v, g, None, state, o, st, ws)
+        return o, st, (q, k, v)
+
+    whole, end, (q, k, v) = attend(0, n, None)
+    o, state, _ = attend(0, prompt, None)
+    outs = [o]
+    for i in range(prompt, n):
+        s, ys = rotated(i, i + 1)
+        y = [t.view(B, H, d) for t in ys]
+        o1 = torch.empty_like(y[0])
+        vdn.vdn_decay_step(s, *y, g, None, state, o1, state)
+        outs.append(o1.view(B, H, 1, 1, d))
+    torch.cuda.synchronize()
+    got = torch.cat(outs, 2)
+    ref, ref_s = tok.decay_attn(_flat(q), _flat(k), _flat(v), _np(g))
+    m, a = tok.decay_scale(_flat(q), _flat(k), _flat(v), _np(g))
+    for t in (whole, got):
+        _near(_flat(t), ref, m, a, dt, n, d)
+    _state_near(_np(state), ref_s)
+    _state_near(_np(end), ref_s)
+
+
+@pytest.mark.parametrize("d,dt", [(128, "bf16"), (64, "bf16"), (32, "f32")])
+def test_prompt_then_tokens(d, dt):
+    _serve(150, 6, 2, 3, d, dt)
+
+
+@pytest.mark.parametrize("n", [100, 2500])
+def test_other_stream_and_graph(n):
+    """On a side stream, and captured: replays follow the inputs, two graphs share a workspace in turn."""
+    x = _inputs(12, 1, 2, 1, n, 128, "bf16", names="qkvo")
+    y = _inputs(13, 1, 2, 1, n, 128, "bf16", names="qkvo", g=x["g"].cpu().numpy())
+    s = vdn.make_shape(1, 2, 1, n, 128, 0)
+    want, want_y = (_attn(s, x), _backward(s, x)), (_attn(s, y), _backward(s, y))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        o, s1 = _attn(s, x)
+    assert torch.equal(o, want[0][0]) and torch.equal(s1, want[0][1])
+    z = {k: t.clone() for k, t in x.items()}
+    ws = vdn.workspace(max(vdn.vdn_decay_attn_workspace_bytes(s), vdn.vdn_decay_attn_backward_workspace_bytes(s)))
+    o, s1, ds = torch.empty_like(z["q"]), torch.empty_like(z["s"]), torch.empty_like(z["s"])
+    grads = [torch.empty_like(z["q"]) for _ in range(3)]
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        vdn.vdn_decay_attn(s, z["q"], z["k"], z["v"], z["g"], None, z["s"], o, s1, ws)
+    with torch.cuda.graph(g2):
+        vdn.vdn_decay_attn_backward(s, z["q"], z["k"], z["v"], z["g"], None, z["s"], z["o"], z["z"], *grads, ds, ws)
+    for src, (fw, bw) in ((x, want), (y, want_y), (x, want)):
+        for k in z:
+            z[k].copy_(src[k])
+        g1.replay()
+        g2.replay()
+        g1.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, fw[0]) and torch.equal(s1, fw[1])
+        assert all(torch.equal(a, b) for a, b in zip(grads, bw[0])) and torch.equal(ds, bw[1])
+
+
+def test_binding_refuses_other_shapes():
+    x = _inputs(14, 1, 2, 1, 20, 64, "bf16")
+    s = vdn.make_shape(1, 2, 1, 20, 64, 0)
+    o, st = torch.empty_like(x["q"]), torch.empty_like(x["s"])
+    ok = [s, x["q"], x["k"], x["v"], x["g"], None, x["s"], o, st, None]
+    for at, bad in ((1, x["q"].float()), (2, x["k"][:, :1]), (4, x["g"].double()), (5, torch.zeros(1, device="cuda")),
+                    (6, x["s"].transpose(2, 3)), (7, o.cpu()), (8, st[:1, :1])):
+        args = list(ok)
+        args[at] = bad
+        with pytest.raises(vdn.VdnError):
+            vdn.vdn_decay_attn(*args)
