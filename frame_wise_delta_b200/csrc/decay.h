@@ -83,6 +83,9 @@ __device__ __forceinline__ double decay_pow(float g, long long n) {
 }
 
 cudaError_t launch_decay_simt(const DecayArgs &a, int in_dtype, int out_dtype, bool sums, cudaStream_t st);
+// bf16 in and out: the tensor cores.
+bool decay_tc_supported(int in_dtype, int out_dtype);
+cudaError_t launch_decay_tc(const DecayArgs &a, bool sums, cudaStream_t st);
 cudaError_t launch_decay_prefix(const DecayArgs &a, cudaStream_t st);
 cudaError_t launch_decay_step(const void *Q, const void *K, const void *V, const float *g, const int32_t *active,
                               const float *s_in, void *O, float *s_out, long long BH, int H, int d, int in_dtype,

@@ -410,8 +410,7 @@ cudaError_t launch_decay_simt(const DecayArgs &a, int in_dtype, int out_dtype, b
                                 : launch_simt_d<float, __nv_bfloat16, false>(a, st);
   }
   if (sums) return launch_simt_d<__nv_bfloat16, float, true>(a, st);
-  return out_dtype == VDN_F32 ? launch_simt_d<__nv_bfloat16, float, false>(a, st)
-                              : launch_simt_d<__nv_bfloat16, __nv_bfloat16, false>(a, st);
+  return out_dtype == VDN_F32 ? launch_simt_d<__nv_bfloat16, float, false>(a, st) : cudaErrorInvalidValue;
 }
 
 cudaError_t launch_decay_prefix(const DecayArgs &a, cudaStream_t st) {

@@ -97,11 +97,15 @@ vdn_status copy_state(const vdn_shape *s, const float *from, float *to, cudaStre
 }
 
 vdn_status run_decay(const vdn_shape *s, DecayArgs &a, cudaStream_t st) {
+  const bool tc = decay_tc_supported(s->in_dtype, s->out_dtype);
+  auto walk = [&](bool sums) {
+    return tc ? launch_decay_tc(a, sums, st) : launch_decay_simt(a, s->in_dtype, s->out_dtype, sums, st);
+  };
   if (a.nseg > 1) {
-    VDN_CUDA(launch_decay_simt(a, s->in_dtype, s->out_dtype, true, st), "decay segment sums");
+    VDN_CUDA(walk(true), "decay segment sums");
     VDN_CUDA(launch_decay_prefix(a, st), "decay segment states");
   }
-  VDN_CUDA(launch_decay_simt(a, s->in_dtype, s->out_dtype, false, st), "decay attention");
+  VDN_CUDA(walk(false), "decay attention");
   return VDN_OK;
 }
 
