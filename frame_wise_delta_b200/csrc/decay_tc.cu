@@ -21,12 +21,15 @@
 // staging tile by TMA. The weighted values enter U as three bf16 parts (2^-24 together): two would
 // leave 3e-6 in the float32 state. P is rounded to bf16 (an error of the size of the output's own).
 //
-// One CTA of 16 warps walks one segment of one (operator, batch, head):
+// One CTA of 32 warps walks one segment of one (operator, batch, head):
 //   warps 0, 1  : scores SC -> P (TMEM lanes 0..63)
 //   warp 2      : TMA producer
 //   warp 3      : TMEM allocation, one lane issues the MMAs
-//   warps 4..11 : the state: lane = value channel (warp % 4), column half (warp - 4) / 4
-//   warps 12..15: the weighted values of the next chunk, then the outputs of this one
+//   warps 4..19 : the state: lane = value channel (warp % 4), column quarter (warp - 4) / 4
+//   warps 20..27: the weighted values: 32 channels (warp % 4), half of them (warp - 20) / 4
+//   warps 28..31: the outputs
+// Many warps with little each: every role is a chain of dependent steps on the way from one chunk
+// to the next, so it is the length of a warp's share that counts.
 // SUMS: only what a segment adds to the state (from zero), for the walk's later segments.
 // Every wait is bounded.
 #include <cudaTypedefs.h>
@@ -39,7 +42,7 @@ namespace vdn {
 namespace {
 
 constexpr int kC = kDecayC;
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr uint32_t kPanel = kC * 128;  // 64 tokens x 64 channels
 constexpr uint32_t kTmemCols = 512;
 
@@ -48,19 +51,23 @@ struct Cfg {
   static constexpr int kPanels = DP / 64;
   static constexpr uint32_t kTile = kPanels * kPanel;
   static constexpr uint32_t kStageBytes = 3 * kTile;  // Q, K, V
-  static constexpr int kStages = DP == 128 ? 4 : 6;
+  static constexpr int kStages = DP == 128 ? 3 : 6;
   // shared memory, from a 1024-byte aligned base; a 128-row operand reads
   // 8 KB past its 64-row tile, which the next tile or P covers
   static constexpr uint32_t kOffP = kStages * kStageBytes;
-  static constexpr uint32_t kOffO = kOffP + kPanel;
-  static constexpr uint32_t kOffTab = kOffO + kTile;
-  static constexpr uint32_t kTabFloats = 2 * 3 * kC + 72 + 4;  // w, c, f per set; l^n; carries
+  static constexpr uint32_t kOffO = kOffP + 2 * kPanel;     // two P, two output tiles
+  static constexpr uint32_t kOffTab = kOffO + 2 * kTile;
+  static constexpr uint32_t kTabFloats = 2 * 3 * kC + 72 + 8;  // w, c, f per set; l^n; carries
   static constexpr uint32_t kOffBar = kOffTab + 4 * kTabFloats;
-  static constexpr uint32_t kBars = 2 * kStages + 11;
+  static constexpr uint32_t kBars = 2 * kStages + 15;
   static constexpr size_t kSmem = 1024 + kOffBar + 8 * kBars + 16;
   // TMEM columns
   static constexpr uint32_t kX = 0, kU = DP, kO = 2 * DP, kSC = kO + kC, kVT = kSC + kC;
-  static_assert(kVT + 3 * kC / 2 <= kTmemCols, "TMEM");
+  static constexpr uint32_t kVTCols = 3 * kC / 2;
+  static_assert(kVT + kVTCols <= kTmemCols, "TMEM");
+  // SUMS: two buffers of U (from column 0) and of the weighted values
+  static constexpr uint32_t kVT2 = 2 * DP;
+  static_assert(kVT2 + 2 * kVTCols <= kTmemCols, "TMEM");
   static_assert(kOffBar % 8 == 0 && kOffTab % 16 == 0, "alignment");
 };
 
@@ -73,15 +80,143 @@ __device__ __forceinline__ void fail(volatile int *abort, int32_t *info) {
   if (info) atomicExch(info, VDN_INFO_TIMEOUT);
 }
 
-// Two values as three bf16 parts each (a in the low halves).
-__device__ __forceinline__ void split3(float a, float b, uint32_t &h, uint32_t &m, uint32_t &l) {
-  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
-  const float ra = a - __low2float(x), rb = b - __high2float(x);
-  const __nv_bfloat162 y = __floats2bfloat162_rn(ra, rb);
-  const __nv_bfloat162 z = __floats2bfloat162_rn(ra - __low2float(y), rb - __high2float(y));
-  h = *reinterpret_cast<const uint32_t *>(&x);
-  m = *reinterpret_cast<const uint32_t *>(&y);
-  l = *reinterpret_cast<const uint32_t *>(&z);
+// mbar_wait with the suspending test (mbarrier.try_wait): with 32 warps in the
+// block, warps that spin take the issue slots of those that work.
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, volatile int *abort) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    if (it == 0) t0 = global_ns();
+    if (global_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+// A whole warp waits.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+  return __all_sync(0xffffffffu, mbar_sleep(bar, parity, abort));
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts_u4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+// Keeps a value from being computed anew at each of its uses.
+__device__ __forceinline__ int pinned(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
+__device__ __forceinline__ uint32_t as_u32(const __nv_bfloat162 &x) { return *reinterpret_cast<const uint32_t *>(&x); }
+// A bf16 pair as two floats (the low half first).
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+}
+// The upper 16 bits of each of x (a bf16 pair); x becomes what they leave. Cut
+// off, not rounded: the next part takes up the rest, exactly, and a byte
+// permutation is cheaper than a conversion.
+__device__ __forceinline__ uint32_t take_bf16(float2 &x) {
+  const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+  x = __ffma2_rn(make_float2(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u)),
+                 make_float2(-1.f, -1.f), x);
+  return __byte_perm(a, b, 0x7632);
+}
+
+// Four transposed 8 x 8 bf16 matrices (lane l: the address of row l % 8 of
+// matrix l / 8). Lane l holds elements (2 (l % 4), l / 4) and (2 (l % 4) + 1,
+// l / 4) of each matrix as it lies in shared memory.
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t &x, uint32_t &y, uint32_t &z, uint32_t &w) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y),
+               "r"(z), "r"(w)
+               : "memory");
+}
+// 16 TMEM lanes x 16 words: register 2 n + e of lane l is lane l / 4 + 8 e,
+// column 4 n + l % 4.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// 32 TMEM lanes x 16 words: lane l's row.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 32 TMEM lanes x 4 words: lane l's row.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+// 16 TMEM lanes x 64 words: registers 4 n + 2 e + c of lane l are lane l / 4 +
+// 8 e, column 8 n + 2 (l % 4) + c.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -97,12 +232,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float *tab = reinterpret_cast<float *>(smem + F::kOffTab);
   float *pw = tab + 2 * 3 * kC;       // l^n, n = 0..64
-  float *carry = pw + 72;             // per set: l^n of its valid rows as two floats
+  float *carry = pw + 72;             // per set: l^n of its valid rows
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + F::kOffBar);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * F::kStages;
   const uint32_t sc_full = empty0 + 8 * F::kStages, sc_free = sc_full + 8, p_ready = sc_free + 8;
-  const uint32_t vt_ready = p_ready + 8, kv_full = vt_ready + 8, u_free = kv_full + 8;
-  const uint32_t x_ready = u_free + 8, qx_done = x_ready + 8, pv_done = qx_done + 8, o_free = pv_done + 8;
+  const uint32_t vt_ready = p_ready + 16, kv_full = vt_ready + 16, u_free = kv_full + 16;  // per buffer
+  const uint32_t x_ready = u_free + 16, qx_done = x_ready + 8, pv_done = qx_done + 8, o_free = pv_done + 8;
   const uint32_t drain = o_free + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + F::kBars);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -110,14 +245,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const DecayWork w = decay_work(p, blockIdx.x);
   const DecayOp &op = p.op[w.op];
-  const int back = op.back;
+  const int back = pinned(op.back);
   const bool fin = w.seg == decay_final_seg(w, back);
   if (SUMS ? !decay_before_final(w, back) : (w.nch == 0 && !fin)) return;
-  const int nch = w.nch, d = p.d;
+  const int nch = pinned(w.nch), d = pinned(p.d);
   const long long DD = (long long)d * d;
-  const int tail = w.end - w.begin - (nch - 1) * kC;  // rows of the segment's last chunk
+  const int tail = pinned(w.end - w.begin - (nch - 1) * kC);  // rows of the segment's last chunk
   const float g = p.g[w.h];
-  const bool steep = (double)g * kC < -41.588830833596719;  // l^64 < 2^-60
+  const int steep = pinned((double)g * kC < -41.588830833596719);  // l^64 < 2^-60
+  const uint32_t smem_a = (uint32_t)pinned((int)smem_u32(smem)), tab_a = smem_a + F::kOffTab;
   auto chunk_at = [&](int it) { return back ? nch - 1 - it : it; };
   auto rows_of = [&](int c) { return c == nch - 1 ? tail : kC; };
 
@@ -128,11 +264,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(sc_full, 1);
     mbar_init(sc_free, 64);
-    mbar_init(p_ready, 64);
-    mbar_init(vt_ready, DP);
-    mbar_init(kv_full, 1);
-    mbar_init(u_free, 2 * DP);
-    mbar_init(x_ready, 2 * DP);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(p_ready + 8 * i, 64);
+      mbar_init(vt_ready + 8 * i, 2 * DP);
+      mbar_init(kv_full + 8 * i, 1);
+      mbar_init(u_free + 8 * i, 4 * DP);
+    }
+    mbar_init(x_ready, 4 * DP);
     mbar_init(qx_done, 1);
     mbar_init(pv_done, 1);
     mbar_init(o_free, DP);
@@ -153,15 +291,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     pw[threadIdx.x - 2 * kC] = (float)decay_pow(g, threadIdx.x - 2 * kC);
   } else if (threadIdx.x >= 256 && threadIdx.x < 258) {
     const int set = threadIdx.x - 256;
+    // l^n lies between two neighbouring floats; taking the upper one for this
+    // share of the chunks keeps the product over many chunks from drifting
     const double l = decay_pow(g, set ? tail : kC);
-    carry[2 * set] = (float)l;
-    carry[2 * set + 1] = (float)(l - (double)(float)l);
+    const float lo = __double2float_rd(l), hi = __double2float_ru(l);
+    carry[4 * set] = lo;
+    carry[4 * set + 1] = hi;
+    carry[4 * set + 2] = __uint_as_float(hi > lo ? __double2uint_rn((l - lo) / ((double)hi - lo) * 4294967295.0) : 0u);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto set_of = [&](int c) { return c == nch - 1 ? 1 : 0; };
+  // buffers of U and of the weighted values: TMEM holds two without the outputs' operands
+  constexpr int kBuf = SUMS ? 2 : 1;
+  auto buf = [](int it) { return it % kBuf; };
+  auto phase = [](int it) { return (uint32_t)((it / kBuf) & 1); };
+  auto u_at = [&](int it) { return tmem + (SUMS ? (uint32_t)(buf(it) * DP) : F::kU); };
+  auto vt_at = [&](int it) { return tmem + (SUMS ? F::kVT2 + (uint32_t)buf(it) * F::kVTCols : F::kVT); };
 
   if (warp == 2) {
     // ------------------------------------------------------------- loads
@@ -173,11 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it = 0;
       for (; it < nch; ++it) {
         const int s = it % F::kStages;
-        if (it >= F::kStages && !mbar_wait(empty0 + 8 * s, (uint32_t)((it / F::kStages - 1) & 1), abort)) {
+        if (it >= F::kStages && !mbar_sleep(empty0 + 8 * s, (uint32_t)((it / F::kStages - 1) & 1), abort)) {
           fail(abort, p.info);
           break;
         }
-        const uint32_t dst = smem_u32(smem) + s * F::kStageBytes, fb = full0 + 8 * s;
+        const uint32_t dst = smem_a + s * F::kStageBytes, fb = full0 + 8 * s;
         const int t0 = w.begin + chunk_at(it) * kC;
         mbar_arrive_expect_tx(fb, SUMS ? 2 * F::kTile : F::kStageBytes);
 #pragma unroll
@@ -194,142 +342,167 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 3) {
     // -------------------------------------------------------------- MMAs
-    if (lane == 0) {
-      constexpr uint32_t id_sc = idesc_bf16_f32(128, kC, false, false);
-      constexpr uint32_t id_u = idesc_bf16_f32(128, DP, false, true);
-      constexpr uint32_t id_pv = idesc_bf16_f32(128, kC, true, false);
-      bool ok = true;
-      auto wait = [&](uint32_t bar, int i) {
-        if (ok && !mbar_wait(bar, (uint32_t)(i & 1), abort)) ok = false;
-        tc_fence_after();
-        return ok;
-      };
-      auto base = [&](int it) { return smem_u32(smem) + (it % F::kStages) * F::kStageBytes; };
-      auto wait_full = [&](int it) {
-        if (ok && !mbar_wait(full0 + 8 * (it % F::kStages), (uint32_t)((it / F::kStages) & 1), abort)) ok = false;
-        return ok;
-      };
-      auto scores = [&](int it) {
-        const uint32_t q = base(it), k = q + F::kTile;
+    // The whole warp walks the loop and one elected lane issues: in a branch
+    // of one lane each product would first move its operands to uniform
+    // registers lane by lane (200 cycles a product instead of 35 to 70).
+    constexpr uint32_t id_sc = idesc_bf16_f32(128, kC, false, false);
+    constexpr uint32_t id_u = idesc_bf16_f32(128, DP, false, true);
+    constexpr uint32_t id_pv = idesc_bf16_f32(128, kC, true, false);
+    bool ok = true;
+    auto wait = [&](uint32_t bar, int i) {
+      ok = ok && warp_wait(bar, (uint32_t)(i & 1), abort);
+      tc_fence_after();
+      return ok;
+    };
+    auto wait_full = [&](int it) {
+      ok = ok && warp_wait(full0 + 8 * (it % F::kStages), (uint32_t)((it / F::kStages) & 1), abort);
+      return ok;
+    };
+    // descriptors: one per tile and form; an offset of b bytes adds b / 16
+    const uint64_t kmaj = smem_desc_sw128(smem_a, 16, 1024), mnmaj = smem_desc_sw128(smem_a, kPanel, 1024);
+    const uint64_t dp = kmaj + (F::kOffP >> 4);
+    auto stage_off = [&](int it) { return (uint64_t)((it % F::kStages) * (F::kStageBytes >> 4)); };
+    auto scores = [&](int it) {
+      const uint64_t q = kmaj + stage_off(it), k = q + (F::kTile >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * kPanel + (ks & 3) * 32;
-          tc_mma_bf16(tmem + F::kSC, smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024), id_sc,
-                      ks > 0 ? 1u : 0u);
+          const uint32_t off = ((ks >> 2) * kPanel + (ks & 3) * 32) >> 4;
+          tc_mma_bf16(tmem + F::kSC, q + off, k + off, id_sc, ks > 0 ? 1u : 0u);
         }
         tc_commit(sc_full);
-      };
-      if (!SUMS && nch > 0 && wait_full(0)) scores(0);
-      for (int it = 0; it < nch && ok; ++it) {
-        const uint32_t q = base(it), k = q + F::kTile, v = k + F::kTile;
-        // U = (w v)^T K, the smallest parts first
-        if (SUMS && !wait_full(it)) break;
-        if (!wait(vt_ready, it) || (it > 0 && !wait(u_free, it - 1))) break;
+      }
+      __syncwarp();
+    };
+    if (!SUMS && nch > 0 && wait_full(0)) scores(0);
+    for (int it = 0; it < nch && ok; ++it) {
+      const uint64_t so = stage_off(it);
+      const uint32_t empty = empty0 + 8 * (it % F::kStages);
+      // U = (w v)^T K, the smallest parts first
+      if (SUMS && !wait_full(it)) break;
+      ok = warp_wait(vt_ready + 8 * buf(it), phase(it), abort);
+      if (ok && it >= kBuf) ok = warp_wait(u_free + 8 * buf(it), phase(it - kBuf), abort);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t k = mnmaj + so + (F::kTile >> 4);
+      const uint32_t u = u_at(it), vt = vt_at(it);
+      if (elect_one()) {
 #pragma unroll
         for (int part = 2; part >= 0; --part)
 #pragma unroll
           for (int ks = 0; ks < kC / 16; ++ks)
-            tc_mma_bf16_ts(tmem + F::kU, tmem + F::kVT + part * (kC / 2) + 8 * ks,
-                           smem_desc_sw128(k + ks * 2048, kPanel, 1024), id_u, part < 2 || ks > 0 ? 1u : 0u);
-        tc_commit(kv_full);
-        if (SUMS) {
-          tc_commit(empty0 + 8 * (it % F::kStages));
-          continue;
-        }
-        // O = X Q^T
-        if (!wait(x_ready, it) || (it > 0 && !wait(o_free, it - 1))) break;
+            tc_mma_bf16_ts(u, vt + part * (kC / 2) + 8 * ks, k + ks * (2048 >> 4), id_u, part < 2 || ks > 0 ? 1u : 0u);
+        tc_commit(kv_full + 8 * buf(it));
+        if (SUMS) tc_commit(empty);
+      }
+      __syncwarp();
+      if (SUMS) continue;
+      // the next chunk's scores, so that its P is made under this one's outputs
+      if (it + 1 < nch) {
+        if (!wait_full(it + 1) || !wait(sc_free, it)) break;
+        scores(it + 1);
+      }
+      // O = X Q^T
+      if (!wait(x_ready, it) || (it > 0 && !wait(o_free, it - 1))) break;
+      const uint64_t q = kmaj + so;
+      if (elect_one()) {
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int ks = 0; ks < DP / 16; ++ks)
             tc_mma_bf16_ts(tmem + F::kO, tmem + F::kX + part * (DP / 2) + 8 * ks,
-                           smem_desc_sw128(q + (ks >> 2) * kPanel + (ks & 3) * 32, 16, 1024), id_sc,
-                           part > 0 || ks > 0 ? 1u : 0u);
+                           q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4), id_sc, part > 0 || ks > 0 ? 1u : 0u);
         tc_commit(qx_done);
-        // the next chunk's scores run while this one's P is made
-        if (it + 1 < nch) {
-          if (!wait_full(it + 1) || !wait(sc_free, it)) break;
-          scores(it + 1);
-        }
-        // O += V^T P^T
-        if (!wait(p_ready, it)) break;
+      }
+      __syncwarp();
+      // O += V^T P^T
+      if (!wait(p_ready + 8 * (it & 1), it >> 1)) break;
+      const uint64_t v = mnmaj + so + (2 * F::kTile >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < kC / 16; ++ks)
-          tc_mma_bf16(tmem + F::kO, smem_desc_sw128(v + ks * 2048, kPanel, 1024),
-                      smem_desc_sw128(smem_u32(smem + F::kOffP) + ks * 32, 16, 1024), id_pv, 1u);
+          tc_mma_bf16(tmem + F::kO, v + ks * (2048 >> 4), dp + (it & 1) * (kPanel >> 4) + ks * (32 >> 4), id_pv, 1u);
         tc_commit(pv_done);
-        tc_commit(empty0 + 8 * (it % F::kStages));
+        tc_commit(empty);
       }
-      if (!ok) fail(abort, p.info);
-      volatile int never = 0;
-      tc_commit(drain);
-      mbar_wait(drain, 0, &never);
+      __syncwarp();
     }
+    if (!ok) fail(abort, p.info);
+    if (elect_one()) tc_commit(drain);
+    __syncwarp();
+    volatile int never = 0;
+    warp_wait(drain, 0, &never);
   } else if (warp < 2) {
     // ----------------------------------------------- scores -> P (row i)
     if (!SUMS) {
       const int i = warp * 32 + lane;
       const uint32_t at = tmem + F::kSC + ((uint32_t)(warp * 32) << 16);
-      uint8_t *row = smem + F::kOffP + i * 128;
+      const uint32_t row0 = smem_a + F::kOffP + i * 128;
+      const uint32_t pw_a = tab_a + 4 * 2 * 3 * kC;
+      // of the tile's four 32 x 32 blocks one lies outside of every mask: it is
+      // cleared once
+      const int skip = back ? (warp == 1 ? 0 : -1) : (warp == 0 ? 1 : -1);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        sts_u4(row0 + 16 * x, 0, 0, 0, 0);
+        sts_u4(row0 + kPanel + 16 * x, 0, 0, 0, 0);
+      }
+      __syncwarp();
       for (int it = 0; it < nch; ++it) {
         const int c = chunk_at(it), n = rows_of(c);
-        const float *t = tab + set_of(c) * 3 * kC;
-        if (!__all_sync(0xffffffffu, mbar_wait(sc_full, (uint32_t)(it & 1), abort))) {
+        const uint32_t t = tab_a + set_of(c) * (3 * kC * 4), row = row0 + (it & 1) * kPanel;
+        // the columns this row takes
+        const uint64_t upto = (2ull << i) - 1, rows = n < kC ? (1ull << n) - 1 : ~0ull;
+        const uint64_t mask = back ? rows & ~(upto >> 1) : upto;
+        // once these scores are done, so is the product that read this P buffer;
+        // the one before it may still wait for its own, so each has its barrier
+        if (!warp_wait(sc_full, (uint32_t)(it & 1), abort)) {
           fail(abort, p.info);
           break;
         }
         tc_fence_after();
-        uint32_t pk[kC / 2];
-        const float rf = steep ? 1.f / t[2 * kC + i] : 0.f;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float v[32];
-          tmem_ld32(at + 32 * b, v);
-          if (b == 1) {
-            tc_fence_before();
-            mbar_arrive(sc_free);
+        for (int b = 0; b < 4; ++b) {
+          if ((b >> 1) == skip) continue;
+          float v[16];
+          tmem_ld16(at + 16 * b, v);
+          const uint32_t m = (uint32_t)(mask >> (16 * b));
+          if (steep) {
+            const int ii = pinned(i);  // addresses made here, not kept for all columns
+            const float rf = 1.f / lds_f(t + 4 * (2 * kC + ii));
+#pragma unroll
+            for (int x = 0; x < 16; ++x) v[x] *= rf * lds_f(pw_a + 4 * abs(ii - 16 * b - x));
+          } else {
+#pragma unroll
+            for (int x = 0; x < 16; x += 4) {
+              const float4 c4 = lds_f4(t + 4 * (kC + 16 * b + x));
+              const float2 y = __fmul2_rn(make_float2(v[x], v[x + 1]), make_float2(c4.x, c4.y));
+              const float2 z = __fmul2_rn(make_float2(v[x + 2], v[x + 3]), make_float2(c4.z, c4.w));
+              v[x] = y.x, v[x + 1] = y.y, v[x + 2] = z.x, v[x + 3] = z.y;
+            }
           }
 #pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            const int j = 32 * b + x;
-            float cj[4];
-            if (steep) {
+          for (int x = 0; x < 16; x += 8) {
+            uint32_t pk[4];
 #pragma unroll
-              for (int y = 0; y < 4; ++y) cj[y] = rf * pw[abs(i - j - y)];
-            } else {
-              const float4 c4 = *reinterpret_cast<const float4 *>(t + kC + j);
-              cj[0] = c4.x, cj[1] = c4.y, cj[2] = c4.z, cj[3] = c4.w;
-            }
-            float r[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const bool in = back ? (j + y >= i && j + y < n) : j + y <= i;
-              r[y] = in ? v[x + y] * cj[y] : 0.f;
-            }
-            pk[j / 2] = pack_bf16(r[0], r[1]);
-            pk[j / 2 + 1] = pack_bf16(r[2], r[3]);
+            for (int e = 0; e < 4; ++e)
+              pk[e] = pack_bf16(m & (1u << (x + 2 * e)) ? v[x + 2 * e] : 0.f, m & (2u << (x + 2 * e)) ? v[x + 2 * e + 1] : 0.f);
+            sts_u4(row + (((2 * b + x / 8) ^ (i & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
           }
         }
-        // the previous chunk's product has read P
-        if (it > 0 && !__all_sync(0xffffffffu, mbar_wait(pv_done, (uint32_t)((it - 1) & 1), abort))) {
-          fail(abort, p.info);
-          break;
-        }
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          *reinterpret_cast<uint4 *>(row + ((x ^ (i & 7)) << 4)) =
-              make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+        tc_fence_before();
+        mbar_arrive(sc_free);
         fence_proxy_async_smem();
-        mbar_arrive(p_ready);
+        mbar_arrive(p_ready + 8 * (it & 1));
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < 20) {
     // --------------------------------------------------------- the state
-    const int sub = warp & 3, half = (warp - 4) >> 2;
-    const int r = sub * 32 + lane, c0 = half * (DP / 2);  // value channel, first key channel
+    const int sub = warp & 3, part = (warp - 4) >> 2;
+    const int r = sub * 32 + lane, c0 = part * (DP / 4);  // value channel, first key channel
     const uint32_t lanes = (uint32_t)(sub * 32) << 16;
     if (sub * 32 < DP) {
-      float X[DP / 2];
+      float2 X[DP / 8];
       const float *src = nullptr;
       bool tr = false;
       if (!SUMS) {
@@ -340,27 +513,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           tr = op.s_in_t;
         }
       }
+      const int sr = tr ? 1 : d, sc = tr ? d : 1;  // strides of a state's row and column
 #pragma unroll
-      for (int x = 0; x < DP / 2; x += 4) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (src && r < d && c0 + x < d) {
-          if (tr) {
-            const float *z = src + (c0 + x) * d + r;
-            y = make_float4(z[0], z[d], z[2 * d], z[3 * d]);
-          } else {
-            y = *reinterpret_cast<const float4 *>(src + r * d + c0 + x);
-          }
+      for (int x = 0; x < DP / 8; ++x) {
+        X[x] = make_float2(0.f, 0.f);
+        if (src && r < d && c0 + 2 * x < d) {
+          const float *y = src + r * sr + (c0 + 2 * x) * sc;
+          X[x] = make_float2(y[0], y[sc]);
         }
-        X[x] = y.x, X[x + 1] = y.y, X[x + 2] = y.z, X[x + 3] = y.w;
       }
       auto publish = [&] {
 #pragma unroll
-        for (int b = 0; b < DP / 64; ++b) {
-          uint32_t hi[16], lo[16];
+        for (int b = 0; b < DP / 32; ++b) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int x = 0; x < 16; ++x) split_bf16x2(X[32 * b + 2 * x], X[32 * b + 2 * x + 1], hi[x], lo[x]);
-          tmem_st16(tmem + lanes + F::kX + half * (DP / 4) + 16 * b, hi);
-          tmem_st16(tmem + lanes + F::kX + DP / 2 + half * (DP / 4) + 16 * b, lo);
+          for (int x = 0; x < 4; ++x) {
+            float2 y = X[4 * b + x];
+            asm volatile("" : "+f"(y.x), "+f"(y.y));  // block by block: fewer registers at once
+            hi[x] = take_bf16(y);
+            lo[x] = as_u32(__floats2bfloat162_rn(y.x, y.y));
+          }
+          tmem_st4(tmem + lanes + F::kX + part * (DP / 8) + 4 * b, hi);
+          tmem_st4(tmem + lanes + F::kX + DP / 2 + part * (DP / 8) + 4 * b, lo);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -368,151 +542,188 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (!SUMS && nch > 0) publish();
       bool ok = true;
+      uint32_t turn = 0x80000000u;
       for (int it = 0; it < nch; ++it) {
-        const float l0 = carry[2 * set_of(chunk_at(it))], l1 = carry[2 * set_of(chunk_at(it)) + 1];
-        ok = __all_sync(0xffffffffu, mbar_wait(kv_full, (uint32_t)(it & 1), abort));
+        const float4 ca = lds_f4(tab_a + 4 * (2 * 3 * kC + 72 + 4 * set_of(chunk_at(it))));
+        const uint32_t before = turn;
+        turn += __float_as_uint(ca.z);
+        const float ll = turn < before ? ca.y : ca.x;
+        const float2 l = make_float2(ll, ll);
+        ok = warp_wait(kv_full + 8 * buf(it), phase(it), abort);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < DP / 64; ++b) {
-          float u[32];
-          tmem_ld32(tmem + lanes + F::kU + c0 + 32 * b, u);
+        for (int b = 0; b < DP / 32; ++b) {
+          float u[8];
+          tmem_ld8(u_at(it) + lanes + c0 + 8 * b, u);
 #pragma unroll
-          for (int x = 0; x < 32; ++x) X[32 * b + x] = fmaf(X[32 * b + x], l0, fmaf(X[32 * b + x], l1, u[x]));
+          for (int x = 0; x < 4; ++x) {
+            float2 &y = X[4 * b + x];
+            y = __ffma2_rn(y, l, make_float2(u[2 * x], u[2 * x + 1]));
+          }
         }
         tc_fence_before();
-        mbar_arrive(u_free);
+        mbar_arrive(u_free + 8 * buf(it));
         if (!SUMS && it + 1 < nch) {
-          ok = __all_sync(0xffffffffu, mbar_wait(qx_done, (uint32_t)(it & 1), abort));
+          ok = warp_wait(qx_done, (uint32_t)(it & 1), abort);
           if (!ok) break;
           tc_fence_after();
           publish();
         }
       }
       if (!ok) fail(abort, p.info);
-      float *dst = SUMS ? p.ws + (long long)blockIdx.x * DD : (fin && op.s_out ? op.s_out + w.bh * DD : nullptr);
-      if (dst && r < d) {
+      // where it goes is found anew: kept over the loop, it would cost registers
+      const int tid = pinned((int)threadIdx.x), blk = pinned((int)blockIdx.x), r1 = tid & 127, c1 = ((tid >> 7) - 1) * (DP / 4);
+      const DecayWork w1 = decay_work(p, blk);
+      const DecayOp &op1 = p.op[w1.op];
+      float *dst = nullptr;
+      if (SUMS)
+        dst = p.ws + (long long)blk * p.d * p.d;
+      else if (w1.seg == decay_final_seg(w1, op1.back) && op1.s_out)
+        dst = op1.s_out + w1.bh * (long long)p.d * p.d;
+      if (dst && r1 < p.d) {
 #pragma unroll
-        for (int x = 0; x < DP / 2; x += 4)
-          if (c0 + x < d)
-            *reinterpret_cast<float4 *>(dst + r * d + c0 + x) = make_float4(X[x], X[x + 1], X[x + 2], X[x + 3]);
+        for (int x = 0; x < DP / 4; x += 4)
+          if (c1 + x < p.d)
+            *reinterpret_cast<float4 *>(dst + r1 * p.d + c1 + x) =
+                make_float4(X[x / 2].x, X[x / 2].y, X[x / 2 + 1].x, X[x / 2 + 1].y);
       }
     }
   } else {
-    // ------------------------------------- weighted values, then outputs
-    const int sub = warp & 3, r = sub * 32 + lane;  // value channel
-    const uint32_t lanes = (uint32_t)(sub * 32) << 16;
+    // -------------------------------------- weighted values and outputs
+    // In fragments of 16 channels x 16 tokens: ldmatrix and stmatrix transpose
+    // between the tiles (rows = tokens) and TMEM (lanes = channels).
+    const int sub = warp & 3;
     if (sub * 32 < DP) {
-      // byte offset of (token x, this channel) in a swizzled tile: col[x & 7] + 128 x
-      uint32_t col[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        col[x] = (uint32_t)(r >> 6) * kPanel + ((((uint32_t)(r & 63) >> 3) ^ (uint32_t)x) << 4) + (uint32_t)(r & 7) * 2u;
       bool ok = true;
-      const int gt = threadIdx.x - 384;
-      uint8_t *ob = smem + F::kOffO;
-      auto values = [&](int it) {
+      const int gt = (int)threadIdx.x - 896;  // thread of the outputs' warps
+      const uint32_t ob0 = smem_a + F::kOffO, lanes = (uint32_t)(sub * 32) << 16;
+      // this lane's matrix row: token 8 (lane / 16) + lane % 8 of a pair of
+      // token groups, channels 8 ((lane / 8) % 2) .. of a group of 16
+      auto row_at = [&](int h) {
+        const uint32_t ch = (uint32_t)(sub * 4 + h * 2 + ((lane >> 3) & 1));  // group of 8 channels
+        return (ch >> 3) * kPanel + (uint32_t)((lane >> 4) * 8 + (lane & 7)) * 128u + (((ch & 7) ^ (uint32_t)(lane & 7)) << 4);
+      };
+      const int tok = 2 * (lane & 3);  // this lane's tokens: 8 n + tok, + 1
+      auto values = [&](int it, int h, uint32_t at) {
         const int s = it % F::kStages, c = chunk_at(it), n = rows_of(c);
-        uint8_t *v = smem + s * F::kStageBytes + 2 * F::kTile;
-        const float *wt = tab + set_of(c) * 3 * kC;
-        ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, (uint32_t)((it / F::kStages) & 1), abort));
+        const uint32_t v = smem_a + s * F::kStageBytes + 2 * F::kTile;
+        const uint32_t wt = tab_a + set_of(c) * (3 * kC * 4) + 4 * tok;
+        ok = warp_wait(full0 + 8 * s, (uint32_t)((it / F::kStages) & 1), abort);
         if (!ok) return;
-        // the previous chunk's U has read the weighted values
-        if (it > 0) ok = __all_sync(0xffffffffu, mbar_wait(kv_full, (uint32_t)((it - 1) & 1), abort));
-        if (!ok) return;
-        tc_fence_after();
+        uint32_t x[16];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          uint32_t h[16], m[16], l[16];
+        for (int e = 0; e < 4; ++e) ldsm4t(v + at + e * 2048, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        if (n < kC) {
 #pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            const int j = 32 * b + x;
-            const float4 w4 = *reinterpret_cast<const float4 *>(wt + j);
-            float y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[e] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(v + col[(j + e) & 7] + 128 * (j + e)) << 16);
-            y[0] *= w4.x, y[1] *= w4.y, y[2] *= w4.z, y[3] *= w4.w;
-            if (n < kC) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = j + e < n ? y[e] : 0.f;
-            }
-            split3(y[0], y[1], h[x / 2], m[x / 2], l[x / 2]);
-            split3(y[2], y[3], h[x / 2 + 1], m[x / 2 + 1], l[x / 2 + 1]);
+          for (int e = 0; e < 16; ++e) {
+            const int j = 8 * (e >> 1) + tok;
+            x[e] = j + 1 < n ? x[e] : j < n ? x[e] & 0xFFFFu : 0u;
           }
-          tmem_st16(tmem + lanes + F::kVT + 16 * b, h);
-          tmem_st16(tmem + lanes + F::kVT + kC / 2 + 16 * b, m);
-          tmem_st16(tmem + lanes + F::kVT + kC + 16 * b, l);
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t m[8], l[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int g8 = 4 * half + e;  // token group
+            const float2 w2 = lds_f2(wt + 32 * g8);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float2 y = __fmul2_rn(unpack2(x[2 * g8 + q]), w2);
+              x[2 * g8 + q] = take_bf16(y);
+              m[2 * e + q] = take_bf16(y);
+              l[2 * e + q] = as_u32(__floats2bfloat162_rn(y.x, y.y));
+            }
+          }
+          // the U of the chunk before in this buffer has read its weighted values
+          if (half == 0 && it >= kBuf) {
+            ok = warp_wait(kv_full + 8 * buf(it), phase(it - kBuf), abort);
+            if (!ok) return;
+            tc_fence_after();
+          }
+          const uint32_t to = vt_at(it) + lanes + ((uint32_t)(16 * h) << 16) + 16 * half;
+          tmem_st_frag(to, &x[8 * half]);
+          tmem_st_frag(to + kC / 2, m);
+          tmem_st_frag(to + kC, l);
         }
         if (n < kC) {
           // what lies behind the sequence's end meets zeros in the products:
-          // it may be no number, so it is cleared (keys and values)
-          for (int x = n; x < kC; ++x) {
-            *reinterpret_cast<uint16_t *>(v + col[x & 7] + 128 * x) = 0;
-            *reinterpret_cast<uint16_t *>(v - F::kTile + col[x & 7] + 128 * x) = 0;
+          // it may be no number, so it is cleared (keys and values; every
+          // warp its own 16 channels, 2 of its lanes to a row)
+          __syncwarp();
+          for (int y = n + (lane >> 1); y < kC; y += 16) {
+            const uint32_t ch = (uint32_t)(sub * 4 + h * 2 + (lane & 1));
+            const uint32_t a = v + (ch >> 3) * kPanel + y * 128 + (((ch & 7) ^ (uint32_t)(y & 7)) << 4);
+            sts_u4(a, 0, 0, 0, 0);
+            sts_u4(a - F::kTile, 0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(vt_ready);
+        mbar_arrive(vt_ready + 8 * buf(it));
       };
-      auto outputs = [&](int it) {
+      auto outputs = [&](int it, uint32_t at0, uint32_t at1) {
         const int c = chunk_at(it), n = rows_of(c), t0 = w.begin + c * kC;
-        const float *f = tab + set_of(c) * 3 * kC + 2 * kC;
-        ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (uint32_t)(it & 1), abort));
-        if (!ok) return;
+        const uint32_t f = tab_a + (set_of(c) * 3 + 2) * kC * 4 + 4 * tok;
+        // the store before the last one has read this staging tile
+        const uint32_t ob = ob0 + (it & 1) * F::kTile;
+        if (gt == 0) bulk_wait_read<1>();
+        asm volatile("bar.sync 1, %0;" ::"n"(DP) : "memory");
+        ok = ok && warp_wait(pv_done, (uint32_t)(it & 1), abort);
         tc_fence_after();
-        uint32_t y[kC / 2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int h = 0; h < 2; ++h) {
+          if (!ok) break;
           float v[32];
-          tmem_ld32(tmem + lanes + F::kO + 32 * b, v);
-          if (b == 1) {
+          tmem_ld_frag(tmem + lanes + ((uint32_t)(16 * h) << 16) + F::kO, v);
+          if (h == 1) {
             tc_fence_before();
             mbar_arrive(o_free);
           }
 #pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            const float4 f4 = *reinterpret_cast<const float4 *>(f + 32 * b + x);
-            y[16 * b + x / 2] = pack_bf16(v[x] * f4.x, v[x + 1] * f4.y);
-            y[16 * b + x / 2 + 1] = pack_bf16(v[x + 2] * f4.z, v[x + 3] * f4.w);
+          for (int e = 0; e < 4; ++e) {
+            uint32_t y[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int m = 2 * e + (q >> 1);
+              const float2 f2 = lds_f2(f + 32 * m);
+              const float2 z = __fmul2_rn(make_float2(v[4 * m + 2 * (q & 1)], v[4 * m + 2 * (q & 1) + 1]), f2);
+              y[q] = as_u32(__floats2bfloat162_rn(z.x, z.y));
+            }
+            stsm4t(ob + (h ? at1 : at0) + e * 2048, y[0], y[1], y[2], y[3]);
           }
         }
-        // the last store has read the staging tile
-        if (gt == 0) bulk_wait_read<0>();
+        fence_proxy_async_smem();
         asm volatile("bar.sync 1, %0;" ::"n"(DP) : "memory");
-#pragma unroll
-        for (int x = 0; x < kC; x += 2) {
-          *reinterpret_cast<uint16_t *>(ob + col[x & 7] + 128 * x) = (uint16_t)y[x / 2];
-          *reinterpret_cast<uint16_t *>(ob + col[(x + 1) & 7] + 128 * (x + 1)) = (uint16_t)(y[x / 2] >> 16);
-        }
         if (n == kC) {
-          fence_proxy_async_smem();
-          asm volatile("bar.sync 1, %0;" ::"n"(DP) : "memory");
-          if (gt == 0) {
+          if (ok && gt == 0) {
 #pragma unroll
             for (int x = 0; x < F::kPanels; ++x)
-              tma_store_3d(&maps.m[op.o], smem_u32(ob) + x * kPanel, 64 * x, t0, (int)w.bh);
+              tma_store_3d(&maps.m[op.o], ob + x * kPanel, 64 * x, t0, (int)w.bh);
             bulk_commit();
           }
-        } else {
+        } else if (ok) {
           // a sequence that ends inside the tile: its rows alone
-          asm volatile("bar.sync 1, %0;" ::"n"(DP) : "memory");
           __nv_bfloat16 *out = (__nv_bfloat16 *)p.t[op.o] + (w.bh * (long long)p.N + t0) * d;
           const int per = d / 8;
           for (int e = gt; e < n * per; e += DP) {
             const int row = e / per, ch = e - row * per;
             *reinterpret_cast<uint4 *>(out + (long long)row * d + ch * 8) =
-                *reinterpret_cast<const uint4 *>(ob + (ch >> 3) * kPanel + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+                lds_u4(ob + (ch >> 3) * kPanel + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
           }
         }
       };
-      for (int it = 0; it < nch && ok; ++it) {
-        values(it);
-        if (!SUMS && ok && it > 0) outputs(it - 1);
+      if (warp < 28) {
+        const int h = (warp - 20) >> 2;
+        const uint32_t at = row_at(h);
+        for (int it = 0; it < nch && ok; ++it) values(it, h, at);
+      } else if (!SUMS) {
+        const uint32_t at0 = row_at(0), at1 = row_at(1);
+        // after a failed wait: keep the barriers, skip the work
+        for (int it = 0; it < nch; ++it) outputs(it, at0, at1);
       }
-      if (!SUMS && ok && nch > 0) outputs(nch - 1);
       if (!ok) fail(abort, p.info);
       if (gt == 0) bulk_wait_all();
     }
