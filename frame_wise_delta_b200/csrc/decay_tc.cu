@@ -2,29 +2,34 @@
 // + TMA), bf16 in and out, d in {16, 32, 64, 128}; sums and state in float32.
 //
 // Per chunk of 64 tokens (local indexes i, j; n valid rows; X the state in
-// front of it, rows = value channels):
-//   o_i = f_i (X q_i + sum_j c_ij s_ij v_j),   s_ij = q_i . k_j,   c_ij = l^{|i-j|} / f_i
+// front of it, rows = value channels), with s_ij = q_i . k_j and the weights
+// w_j = l^{n-1-j} (back: l^{j+1}) that take a token's write to the chunk's end:
 //   X'  = l^n X + sum_j (w_j v_j) k_j^T
-// forward: j <= i, f_i = l^{i+1}, w_j = l^{n-1-j}; back: j >= i, f_i = l^{n-1-i}, w_j = l^{j+1}. With
-// f_i taken out, c_ij = c_j depends on the column alone (l^{-(j+1)}, or l^{-(n-1-j)} back), and both
-// products share one accumulator. A head that decays by more than 2^-60 over a chunk would overflow
-// there: it takes f_i >= 2^-60 and c_ij entry by entry (the state then enters its late rows with
-// 2^-60 in place of something smaller, far below a rounding of o_i).
+//   o_i = 1/w_i (l^n X q_i + sum_j s_ij w_j v_j),   j <= i (back: j >= i),
+// since l^{i-j} = w_j / w_i and l^{i+1} = l^n / w_i (back: l^{j-i}, l^{n-1-i}). So the weighted values
+// serve both sums, the scores need no weights of their own, and both terms of o_i share one accumulator.
+// 1/w_i is at most 1/l^64. A head that decays by more than 2^-90 over a chunk ("steep") would lose its
+// early values to float32's range: it takes o_i = f_i (X q_i + sum_j c_ij s_ij v_j) with f_i = max(l^{i+1}, 2^-60)
+// (back: l^{n-1-i}) and c_ij = l^{|i-j|} / f_i put on the scores; where f_i is cut off the state enters
+// with 2^-60 in place of something smaller, far below a rounding of o_i.
 //
 // Four products per chunk, all with 128 TMEM lanes:
-//   SC[i][j]  = Q K^T              A = Q, B = K (K-major tiles as TMA brings them; rows 64.. unused)
-//   U[v][k]   = (w v)^T K          A = the weighted values in TMEM, B = K (MN-major)
-//   O[v][i]   = X Q^T + V^T P^T    A = X in TMEM as bf16 hi and lo parts, B = Q; A = V (MN-major),
-//                                  B = P = c SC as bf16, in shared memory
+//   SC[i][j]  = Q K^T                 A = Q, B = K (K-major tiles as TMA brings them; rows 64.. unused)
+//   U[v][k]   = (w V)^T K             A = the weighted values in TMEM, B = K (MN-major)
+//   O[v][i]   = X Q^T + (w V)^T P^T   A = l^n X as bf16 in TMEM, B = Q; A = the weighted values (steep:
+//                                     V, MN-major), B = P = the masked SC as bf16, in shared memory
 // The state stays in registers in float32 and is written to TMEM once per chunk, so it never passes
 // through shared memory; the outputs come transposed (lane = channel) and leave through a swizzled
 // staging tile by TMA. The weighted values enter U as three bf16 parts (2^-24 together): two would
-// leave 3e-6 in the float32 state. P is rounded to bf16 (an error of the size of the output's own).
+// leave 3e-6 in the float32 state. P and the copy of the state that the outputs read are rounded to
+// bf16: each adds an error of the size of the output's own rounding to its share of the output (the
+// sum is 1.4 times the rounding's alone), and a second part of the state would cost a quarter of the
+// chunk's instructions.
 //
 // One CTA of 32 warps walks one segment of one (operator, batch, head):
 //   warps 0, 1  : scores SC -> P (TMEM lanes 0..63)
-//   warp 2      : TMA producer
-//   warp 3      : TMEM allocation, one lane issues the MMAs
+//   warp 2      : TMA loads, the products U
+//   warp 3      : TMEM allocation, the products SC and O
 //   warps 4..19 : the state: lane = value channel (warp % 4), column quarter (warp - 4) / 4
 //   warps 20..27: the weighted values: 32 channels (warp % 4), half of them (warp - 20) / 4
 //   warps 28..31: the outputs
@@ -46,26 +51,27 @@ constexpr int kThreads = 1024;
 constexpr uint32_t kPanel = kC * 128;  // 64 tokens x 64 channels
 constexpr uint32_t kTmemCols = 512;
 
-template <int DP>  // channels padded to panels
+template <int DP, bool SUMS>  // channels padded to panels
 struct Cfg {
   static constexpr int kPanels = DP / 64;
   static constexpr uint32_t kTile = kPanels * kPanel;
-  static constexpr uint32_t kStageBytes = 3 * kTile;  // Q, K, V
-  static constexpr int kStages = DP == 128 ? 3 : 6;
+  static constexpr uint32_t kOffK = SUMS ? 0 : kTile, kOffV = kOffK + kTile;  // in a stage, behind Q
+  static constexpr uint32_t kStageBytes = kOffV + kTile;
+  static constexpr int kStages = SUMS ? 6 : DP == 128 ? 3 : 6;
   // shared memory, from a 1024-byte aligned base; a 128-row operand reads
   // 8 KB past its 64-row tile, which the next tile or P covers
   static constexpr uint32_t kOffP = kStages * kStageBytes;
-  static constexpr uint32_t kOffO = kOffP + 2 * kPanel;     // two P, two output tiles
-  static constexpr uint32_t kOffTab = kOffO + 2 * kTile;
-  static constexpr uint32_t kTabFloats = 2 * 3 * kC + 72 + 8;  // w, c, f per set; l^n; carries
+  static constexpr uint32_t kOffO = kOffP + (SUMS ? 0 : 2 * kPanel);  // two P, two output tiles
+  static constexpr uint32_t kOffTab = kOffO + (SUMS ? 0 : 2 * kTile);
+  static constexpr uint32_t kTabFloats = 2 * 2 * kC + 72 + 8 + 16;  // w, f per set; l^n; carries; l^-n
   static constexpr uint32_t kOffBar = kOffTab + 4 * kTabFloats;
-  static constexpr uint32_t kBars = 2 * kStages + 15;
+  static constexpr uint32_t kBars = 2 * kStages + 14;
   static constexpr size_t kSmem = 1024 + kOffBar + 8 * kBars + 16;
   // TMEM columns
-  static constexpr uint32_t kX = 0, kU = DP, kO = 2 * DP, kSC = kO + kC, kVT = kSC + kC;
-  static constexpr uint32_t kVTCols = 3 * kC / 2;
-  static_assert(kVT + kVTCols <= kTmemCols, "TMEM");
-  // SUMS: two buffers of U (from column 0) and of the weighted values
+  static constexpr uint32_t kX = 0, kU = DP / 2, kO = kU + DP, kSC = kO + kC, kVT = kSC + kC;
+  static constexpr uint32_t kVTCols = 3 * kC / 2;  // of each of two buffers
+  static_assert(kVT + 2 * kVTCols <= kTmemCols, "TMEM");
+  // SUMS: two buffers of U as well (from column 0)
   static constexpr uint32_t kVT2 = 2 * DP;
   static_assert(kVT2 + 2 * kVTCols <= kTmemCols, "TMEM");
   static_assert(kOffBar % 8 == 0 && kOffTab % 16 == 0, "alignment");
@@ -96,6 +102,12 @@ __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, volati
     if (it == 0) t0 = global_ns();
     if (global_ns() - t0 > kWaitLimitNs) return false;
   }
+}
+// Whether a phase is done now, for all lanes; two at a time, so that their
+// latencies (100 cycles and more under load) pass together.
+__device__ __forceinline__ bool warp_test(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb) {
+  const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
+  return __all_sync(0xffffffffu, x && y);
 }
 // A whole warp waits.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
@@ -153,6 +165,11 @@ __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
   return __byte_perm(a, b, 0x7632);
 }
 
+// Bits x and x + 1 of m as masks of the halves of a word.
+__device__ __forceinline__ uint32_t pair_mask(uint32_t m, int x) {
+  return __byte_perm((uint32_t)((int)(m << (31 - x)) >> 31), (uint32_t)((int)(m << (30 - x)) >> 31), 0x5410);
+}
+
 // Four transposed 8 x 8 bf16 matrices (lane l: the address of row l % 8 of
 // matrix l / 8). Lane l holds elements (2 (l % 4), l / 4) and (2 (l % 4) + 1,
 // l / 4) of each matrix as it lies in shared memory.
@@ -174,19 +191,7 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t *r) 
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// 32 TMEM lanes x 16 words: lane l's row.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
+// 32 TMEM lanes x 8 words: lane l's row.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
   uint32_t r[8];
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -196,7 +201,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
-// 32 TMEM lanes x 4 words: lane l's row.
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3])
@@ -227,18 +231,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 template <int DP, bool SUMS>
 __global__ void __launch_bounds__(kThreads, 1)
     decay_tc_kernel(const __grid_constant__ DecayMaps maps, const __grid_constant__ DecayArgs p) {
-  using F = Cfg<DP>;
+  using F = Cfg<DP, SUMS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float *tab = reinterpret_cast<float *>(smem + F::kOffTab);
-  float *pw = tab + 2 * 3 * kC;       // l^n, n = 0..64
+  float *pw = tab + 2 * 2 * kC;       // l^n, n = 0..64
   float *carry = pw + 72;             // per set: l^n of its valid rows
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + F::kOffBar);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * F::kStages;
-  const uint32_t sc_full = empty0 + 8 * F::kStages, sc_free = sc_full + 8, p_ready = sc_free + 8;
-  const uint32_t vt_ready = p_ready + 16, kv_full = vt_ready + 16, u_free = kv_full + 16;  // per buffer
-  const uint32_t x_ready = u_free + 16, qx_done = x_ready + 8, pv_done = qx_done + 8, o_free = pv_done + 8;
-  const uint32_t drain = o_free + 8;
+  const uint32_t sc_full = empty0 + 8 * F::kStages, sc_free = sc_full + 8, p_ready = sc_free + 8;  // p, kv: per buffer
+  const uint32_t kv_ok = p_ready + 16, kv_full = kv_ok + 16, pv_done = kv_full + 16;
+  const uint32_t qx_ok = pv_done + 16, qx_done = qx_ok + 8, drain = qx_done + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + F::kBars);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -252,7 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long DD = (long long)d * d;
   const int tail = pinned(w.end - w.begin - (nch - 1) * kC);  // rows of the segment's last chunk
   const float g = p.g[w.h];
-  const int steep = pinned((double)g * kC < -41.588830833596719);  // l^64 < 2^-60
+  // 0: l^64 >= 2^-90; 1: l^15 >= 2^-100; 2: steeper still
+  const int steep = pinned((double)g * kC >= -62.383246250395077 ? 0 : (double)g * 15 >= -69.3 ? 1 : 2);
   const uint32_t smem_a = (uint32_t)pinned((int)smem_u32(smem)), tab_a = smem_a + F::kOffTab;
   auto chunk_at = [&](int it) { return back ? nch - 1 - it : it; };
   auto rows_of = [&](int c) { return c == nch - 1 ? tail : kC; };
@@ -260,21 +264,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < F::kStages; ++s) {
       mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, SUMS ? 1 : 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(p_ready + 8 * i, 64);
+      mbar_init(kv_ok + 8 * i, 6 * DP);  // the values are there, U has been read
+      mbar_init(kv_full + 8 * i, 1);
+      mbar_init(pv_done + 8 * i, 1);
     }
     mbar_init(sc_full, 1);
     mbar_init(sc_free, 64);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(p_ready + 8 * i, 64);
-      mbar_init(vt_ready + 8 * i, 2 * DP);
-      mbar_init(kv_full + 8 * i, 1);
-      mbar_init(u_free + 8 * i, 4 * DP);
-    }
-    mbar_init(x_ready, 4 * DP);
+    mbar_init(qx_ok, 5 * DP);  // the state is there, O has been read
     mbar_init(qx_done, 1);
-    mbar_init(pv_done, 1);
-    mbar_init(o_free, DP);
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     *abort = 0;
     fence_barrier_init();
   }
@@ -282,13 +284,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the weights of whole chunks (set 0) and of the segment's last one (set 1)
   if (threadIdx.x < 2 * kC) {
     const int set = threadIdx.x / kC, x = threadIdx.x % kC, n = set ? tail : kC;
-    float *t = tab + set * 3 * kC;
-    const int er = back ? n - 1 - x : x + 1, ew = back ? x + 1 : n - 1 - x;
-    t[x] = x < n ? (float)decay_pow(g, ew) : 0.f;
-    t[kC + x] = x < n && !steep ? (float)(1.0 / decay_pow(g, er)) : 0.f;
-    t[2 * kC + x] = x < n ? fmaxf((float)decay_pow(g, er), 0x1p-60f) : 1.f;
+    float *t = tab + set * 2 * kC;
+    const double wx = decay_pow(g, back ? x + 1 : n - 1 - x);
+    t[x] = x < n ? (float)wx : 0.f;
+    t[kC + x] = x >= n ? 1.f : steep ? fmaxf((float)decay_pow(g, back ? n - 1 - x : x + 1), 0x1p-60f) : (float)(1.0 / wx);
   } else if (threadIdx.x < 2 * kC + kC + 1) {
     pw[threadIdx.x - 2 * kC] = (float)decay_pow(g, threadIdx.x - 2 * kC);
+  } else if (threadIdx.x >= 224 && threadIdx.x < 240) {
+    const int x = threadIdx.x - 224;
+    carry[8 + x] = steep == 1 ? (float)(1.0 / decay_pow(g, back ? 15 - x : x)) : 0.f;
   } else if (threadIdx.x >= 256 && threadIdx.x < 258) {
     const int set = threadIdx.x - 256;
     // l^n lies between two neighbouring floats; taking the upper one for this
@@ -299,135 +303,168 @@ __global__ void __launch_bounds__(kThreads, 1)
     carry[4 * set + 1] = hi;
     carry[4 * set + 2] = __uint_as_float(hi > lo ? __double2uint_rn((l - lo) / ((double)hi - lo) * 4294967295.0) : 0u);
   }
+  if (!SUMS)
+    for (uint32_t x = threadIdx.x; x < 2 * kPanel / 16; x += kThreads) sts_u4(smem_a + F::kOffP + 16 * x, 0, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto set_of = [&](int c) { return c == nch - 1 ? 1 : 0; };
-  // buffers of U and of the weighted values: TMEM holds two without the outputs' operands
-  constexpr int kBuf = SUMS ? 2 : 1;
-  auto buf = [](int it) { return it % kBuf; };
-  auto phase = [](int it) { return (uint32_t)((it / kBuf) & 1); };
-  auto u_at = [&](int it) { return tmem + (SUMS ? (uint32_t)(buf(it) * DP) : F::kU); };
-  auto vt_at = [&](int it) { return tmem + (SUMS ? F::kVT2 + (uint32_t)buf(it) * F::kVTCols : F::kVT); };
+  // two buffers of the weighted values; of U where TMEM has the room
+  constexpr int kBufU = SUMS ? 2 : 1;
+  auto buf = [](int it) { return it & 1; };
+  auto phase = [](int it) { return (uint32_t)((it >> 1) & 1); };
+  auto u_at = [&](int it) { return tmem + (SUMS ? (uint32_t)((it & 1) * DP) : F::kU); };
+  auto vt_at = [&](int it) { return tmem + (SUMS ? F::kVT2 : F::kVT) + (uint32_t)(it & 1) * F::kVTCols; };
 
-  if (warp == 2) {
-    // ------------------------------------------------------------- loads
-    if (lane == 0) {
-      const CUtensorMap *mq = &maps.m[op.q], *mk = &maps.m[op.k], *mv = &maps.m[op.v];
-      if (!SUMS) tma_prefetch_desc(mq);
-      tma_prefetch_desc(mk);
-      tma_prefetch_desc(mv);
-      int it = 0;
-      for (; it < nch; ++it) {
-        const int s = it % F::kStages;
-        if (it >= F::kStages && !mbar_sleep(empty0 + 8 * s, (uint32_t)((it / F::kStages - 1) & 1), abort)) {
-          fail(abort, p.info);
-          break;
-        }
-        const uint32_t dst = smem_a + s * F::kStageBytes, fb = full0 + 8 * s;
-        const int t0 = w.begin + chunk_at(it) * kC;
-        mbar_arrive_expect_tx(fb, SUMS ? 2 * F::kTile : F::kStageBytes);
-#pragma unroll
-        for (int x = 0; x < F::kPanels; ++x) {
-          if (!SUMS) tma_load_3d(dst + x * kPanel, mq, fb, 64 * x, t0, (int)w.bh);
-          tma_load_3d(dst + F::kTile + x * kPanel, mk, fb, 64 * x, t0, (int)w.bh);
-          tma_load_3d(dst + 2 * F::kTile + x * kPanel, mv, fb, 64 * x, t0, (int)w.bh);
-        }
-      }
-      // every copy issued lands before the CTA may leave
-      volatile int never = 0;
-      for (int i = it > F::kStages ? it - F::kStages : 0; i < it; ++i)
-        mbar_wait(full0 + 8 * (i % F::kStages), (uint32_t)((i / F::kStages) & 1), &never);
-    }
-  } else if (warp == 3) {
-    // -------------------------------------------------------------- MMAs
-    // The whole warp walks the loop and one elected lane issues: in a branch
-    // of one lane each product would first move its operands to uniform
-    // registers lane by lane (200 cycles a product instead of 35 to 70).
+  if (warp == 2 || warp == 3) {
+    // ------------------------------------------------- loads and products
+    // Two warps issue, so that one's waits pass under the other's products:
+    // warp 2 the loads and U, warp 3 the scores and the outputs (with SUMS the
+    // loads). A whole warp
+    // walks its loop and one elected lane issues: in a branch of one lane each
+    // product would first move its operands to uniform registers lane by lane
+    // (200 cycles a product instead of 35 to 70).
     constexpr uint32_t id_sc = idesc_bf16_f32(128, kC, false, false);
     constexpr uint32_t id_u = idesc_bf16_f32(128, DP, false, true);
     constexpr uint32_t id_pv = idesc_bf16_f32(128, kC, true, false);
-    bool ok = true;
-    auto wait = [&](uint32_t bar, int i) {
-      ok = ok && warp_wait(bar, (uint32_t)(i & 1), abort);
-      tc_fence_after();
-      return ok;
-    };
-    auto wait_full = [&](int it) {
-      ok = ok && warp_wait(full0 + 8 * (it % F::kStages), (uint32_t)((it / F::kStages) & 1), abort);
-      return ok;
-    };
     // descriptors: one per tile and form; an offset of b bytes adds b / 16
-    const uint64_t kmaj = smem_desc_sw128(smem_a, 16, 1024), mnmaj = smem_desc_sw128(smem_a, kPanel, 1024);
+    // values that the compiler knows to be the same in all lanes stay in uniform registers
+    const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0), sm = smem_u32(smem);
+    const uint64_t kmaj = smem_desc_sw128(sm, 16, 1024), mnmaj = smem_desc_sw128(sm, kPanel, 1024);
     const uint64_t dp = kmaj + (F::kOffP >> 4);
     auto stage_off = [&](int it) { return (uint64_t)((it % F::kStages) * (F::kStageBytes >> 4)); };
-    auto scores = [&](int it) {
-      const uint64_t q = kmaj + stage_off(it), k = q + (F::kTile >> 4);
+    auto empty = [&](int it) { return empty0 + 8 * (it % F::kStages); };
+    auto full = [&](int it) { return full0 + 8 * (it % F::kStages); };
+    auto turn_of = [&](int it) { return (uint32_t)((it / F::kStages) & 1); };
+    auto vt_of = [&](int it) { return tm + (SUMS ? F::kVT2 : F::kVT) + (uint32_t)(it & 1) * F::kVTCols; };
+    bool ok = true;
+    const CUtensorMap *mq = &maps.m[op.q], *mk = &maps.m[op.k], *mv = &maps.m[op.v];
+    auto load = [&](int it) {
+      const uint32_t dst = smem_a + (it % F::kStages) * F::kStageBytes, fb = full(it);
+      const int t0 = w.begin + chunk_at(it) * kC;
       if (elect_one()) {
+        mbar_arrive_expect_tx(fb, F::kStageBytes);
 #pragma unroll
-        for (int ks = 0; ks < DP / 16; ++ks) {
-          const uint32_t off = ((ks >> 2) * kPanel + (ks & 3) * 32) >> 4;
-          tc_mma_bf16(tmem + F::kSC, q + off, k + off, id_sc, ks > 0 ? 1u : 0u);
+        for (int x = 0; x < F::kPanels; ++x) {
+          if (!SUMS) tma_load_3d(dst + x * kPanel, mq, fb, 64 * x, t0, (int)w.bh);
+          tma_load_3d(dst + F::kOffK + x * kPanel, mk, fb, 64 * x, t0, (int)w.bh);
+          tma_load_3d(dst + F::kOffV + x * kPanel, mv, fb, 64 * x, t0, (int)w.bh);
         }
-        tc_commit(sc_full);
       }
       __syncwarp();
     };
-    if (!SUMS && nch > 0 && wait_full(0)) scores(0);
-    for (int it = 0; it < nch && ok; ++it) {
-      const uint64_t so = stage_off(it);
-      const uint32_t empty = empty0 + 8 * (it % F::kStages);
-      // U = (w v)^T K, the smallest parts first
-      if (SUMS && !wait_full(it)) break;
-      ok = warp_wait(vt_ready + 8 * buf(it), phase(it), abort);
-      if (ok && it >= kBuf) ok = warp_wait(u_free + 8 * buf(it), phase(it - kBuf), abort);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t k = mnmaj + so + (F::kTile >> 4);
-      const uint32_t u = u_at(it), vt = vt_at(it);
-      if (elect_one()) {
+    // every copy issued lands before the CTA may leave
+    auto land = [&](int loaded) {
+      volatile int never = 0;
+      for (int i = loaded > F::kStages ? loaded - F::kStages : 0; i < loaded; ++i) warp_wait(full(i), turn_of(i), &never);
+    };
+    if (warp == 2) {
+      int loaded = 0;
+      if (!SUMS)
+        for (; loaded < nch && loaded < F::kStages; ++loaded) load(loaded);
+      for (int it = 0; it < nch; ++it) {
+        // U = (w v)^T K, the smallest parts first (the values' warps have seen the tile arrive)
+        ok = warp_wait(kv_ok + 8 * buf(it), phase(it), abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t k = mnmaj + stage_off(it) + (F::kOffK >> 4);
+        const uint32_t u = tm + (SUMS ? (uint32_t)((it & 1) * DP) : F::kU), vt = vt_of(it);
+        if (elect_one()) {
 #pragma unroll
-        for (int part = 2; part >= 0; --part)
+          for (int part = 2; part >= 0; --part)
 #pragma unroll
-          for (int ks = 0; ks < kC / 16; ++ks)
-            tc_mma_bf16_ts(u, vt + part * (kC / 2) + 8 * ks, k + ks * (2048 >> 4), id_u, part < 2 || ks > 0 ? 1u : 0u);
-        tc_commit(kv_full + 8 * buf(it));
-        if (SUMS) tc_commit(empty);
+            for (int ks = 0; ks < kC / 16; ++ks)
+              tc_mma_bf16_ts(u, vt + part * (kC / 2) + 8 * ks, k + ks * (2048 >> 4), id_u, part < 2 || ks > 0 ? 1u : 0u);
+          tc_commit(kv_full + 8 * buf(it));
+          tc_commit(empty(it));
+        }
+        __syncwarp();
+        // the stage of the chunk before takes the next load
+        if (!SUMS && it > 0 && loaded < nch) {
+          ok = warp_wait(empty(it - 1), turn_of(it - 1), abort);
+          if (!ok) break;
+          load(loaded++);
+        }
       }
-      __syncwarp();
-      if (SUMS) continue;
-      // the next chunk's scores, so that its P is made under this one's outputs
-      if (it + 1 < nch) {
-        if (!wait_full(it + 1) || !wait(sc_free, it)) break;
-        scores(it + 1);
+      if (!ok) fail(abort, p.info);
+      if (!SUMS) land(loaded);
+    } else if (SUMS) {
+      int loaded = 0;
+      for (; loaded < nch && ok; ++loaded) {
+        if (loaded >= F::kStages) ok = warp_wait(empty(loaded), turn_of(loaded - F::kStages), abort);
+        if (!ok) break;
+        load(loaded);
       }
-      // O = X Q^T
-      if (!wait(x_ready, it) || (it > 0 && !wait(o_free, it - 1))) break;
-      const uint64_t q = kmaj + so;
-      if (elect_one()) {
+      if (!ok) fail(abort, p.info);
+      land(loaded);
+    } else {
+      auto scores = [&](int it) {
+        const uint64_t q = kmaj + stage_off(it), k = q + (F::kOffK >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+          for (int ks = 0; ks < DP / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * kPanel + (ks & 3) * 32) >> 4;
+            tc_mma_bf16(tm + F::kSC, q + off, k + off, id_sc, ks > 0 ? 1u : 0u);
+          }
+          tc_commit(sc_full);
+        }
+        __syncwarp();
+      };
+      if (nch > 0) {
+        ok = warp_wait(full(0), 0, abort);
+        if (ok) scores(0);
+      }
+      for (int it = 0; it < nch && ok; ++it) {
+        // the next chunk's scores, so that its P is made under this one's outputs
+        if (it + 1 < nch) {
+          if (!warp_test(full(it + 1), turn_of(it + 1), sc_free, (uint32_t)(it & 1)))
+            ok = warp_wait(full(it + 1), turn_of(it + 1), abort) && warp_wait(sc_free, (uint32_t)(it & 1), abort);
+          if (!ok) break;
+          tc_fence_after();
+          scores(it + 1);
+        }
+        // O = X Q^T
+        ok = warp_wait(qx_ok, (uint32_t)(it & 1), abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t q = kmaj + stage_off(it);
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < DP / 16; ++ks)
-            tc_mma_bf16_ts(tmem + F::kO, tmem + F::kX + part * (DP / 2) + 8 * ks,
-                           q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4), id_sc, part > 0 || ks > 0 ? 1u : 0u);
-        tc_commit(qx_done);
-      }
-      __syncwarp();
-      // O += V^T P^T
-      if (!wait(p_ready + 8 * (it & 1), it >> 1)) break;
-      const uint64_t v = mnmaj + so + (2 * F::kTile >> 4);
-      if (elect_one()) {
+            tc_mma_bf16_ts(tm + F::kO, tm + F::kX + 8 * ks, q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4), id_sc,
+                           ks > 0 ? 1u : 0u);
+          tc_commit(qx_done);
+        }
+        __syncwarp();
+        // O += (w V)^T P^T (a steep head: V^T P^T)
+        if (!warp_test(p_ready + 8 * (it & 1), phase(it), kv_ok + 8 * (it & 1), phase(it)))
+          ok = warp_wait(p_ready + 8 * (it & 1), phase(it), abort) && warp_wait(kv_ok + 8 * (it & 1), phase(it), abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t pb = dp + (it & 1) * (kPanel >> 4);
+        const uint64_t v = mnmaj + stage_off(it) + (F::kOffV >> 4);
+        const uint32_t vt = vt_of(it);
+        if (elect_one()) {
+          if (steep) {
 #pragma unroll
-        for (int ks = 0; ks < kC / 16; ++ks)
-          tc_mma_bf16(tmem + F::kO, v + ks * (2048 >> 4), dp + (it & 1) * (kPanel >> 4) + ks * (32 >> 4), id_pv, 1u);
-        tc_commit(pv_done);
-        tc_commit(empty);
+            for (int ks = 0; ks < kC / 16; ++ks)
+              tc_mma_bf16(tm + F::kO, v + ks * (2048 >> 4), pb + ks * (32 >> 4), id_pv, 1u);
+          } else {
+#pragma unroll
+            for (int part = 1; part >= 0; --part)
+#pragma unroll
+              for (int ks = 0; ks < kC / 16; ++ks)
+                tc_mma_bf16_ts(tm + F::kO, vt + part * (kC / 2) + 8 * ks, pb + ks * (32 >> 4), id_sc, 1u);
+          }
+          tc_commit(pv_done + 8 * (it & 1));
+          tc_commit(empty(it));
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      if (!ok) fail(abort, p.info);
     }
-    if (!ok) fail(abort, p.info);
+    // every product is done before TMEM is given back
     if (elect_one()) tc_commit(drain);
     __syncwarp();
     volatile int never = 0;
@@ -435,63 +472,63 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 2) {
     // ----------------------------------------------- scores -> P (row i)
     if (!SUMS) {
-      const int i = warp * 32 + lane;
-      const uint32_t at = tmem + F::kSC + ((uint32_t)(warp * 32) << 16);
-      const uint32_t row0 = smem_a + F::kOffP + i * 128;
-      const uint32_t pw_a = tab_a + 4 * 2 * 3 * kC;
-      // of the tile's four 32 x 32 blocks one lies outside of every mask: it is
-      // cleared once
+      // of the tile's four 32 x 32 blocks one lies outside of every mask: it
+      // was cleared at the start
       const int skip = back ? (warp == 1 ? 0 : -1) : (warp == 0 ? 1 : -1);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        sts_u4(row0 + 16 * x, 0, 0, 0, 0);
-        sts_u4(row0 + kPanel + 16 * x, 0, 0, 0, 0);
-      }
-      __syncwarp();
       for (int it = 0; it < nch; ++it) {
+        const int i = pinned(warp * 32 + lane);  // addresses made here, not kept
         const int c = chunk_at(it), n = rows_of(c);
-        const uint32_t t = tab_a + set_of(c) * (3 * kC * 4), row = row0 + (it & 1) * kPanel;
+        const uint32_t t = tab_a + set_of(c) * (2 * kC * 4), pw_a = tab_a + 4 * 2 * 2 * kC;
+        const uint32_t row = smem_a + F::kOffP + (it & 1) * kPanel + i * 128;
         // the columns this row takes
         const uint64_t upto = (2ull << i) - 1, rows = n < kC ? (1ull << n) - 1 : ~0ull;
         const uint64_t mask = back ? rows & ~(upto >> 1) : upto;
-        // once these scores are done, so is the product that read this P buffer;
-        // the one before it may still wait for its own, so each has its barrier
+        // once these scores are done, so is the product that read this P buffer
         if (!warp_wait(sc_full, (uint32_t)(it & 1), abort)) {
           fail(abort, p.info);
           break;
         }
         tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if ((b >> 1) == skip) continue;
-          float v[16];
-          tmem_ld16(at + 16 * b, v);
-          const uint32_t m = (uint32_t)(mask >> (16 * b));
+        for (int b = 0; b < 2; ++b) {
+          if (b == skip) continue;
+          float v[32];
+          tmem_ld32(tmem + F::kSC + ((uint32_t)(warp * 32) << 16) + 32 * b, v);
+          if (b == 1 || skip == 1) {
+            tc_fence_before();
+            mbar_arrive(sc_free);
+          }
           if (steep) {
-            const int ii = pinned(i);  // addresses made here, not kept for all columns
-            const float rf = 1.f / lds_f(t + 4 * (2 * kC + ii));
+            const int ii = pinned(i);
+            const float rf = 1.f / lds_f(t + 4 * (kC + ii));
 #pragma unroll
-            for (int x = 0; x < 16; ++x) v[x] *= rf * lds_f(pw_a + 4 * abs(ii - 16 * b - x));
-          } else {
+            for (int q = 0; q < 32; q += 16) {
+              if (steep == 2) {
 #pragma unroll
-            for (int x = 0; x < 16; x += 4) {
-              const float4 c4 = lds_f4(t + 4 * (kC + 16 * b + x));
-              const float2 y = __fmul2_rn(make_float2(v[x], v[x + 1]), make_float2(c4.x, c4.y));
-              const float2 z = __fmul2_rn(make_float2(v[x + 2], v[x + 3]), make_float2(c4.z, c4.w));
-              v[x] = y.x, v[x + 1] = y.y, v[x + 2] = z.x, v[x + 3] = z.y;
+                for (int x = 0; x < 16; ++x) v[q + x] *= rf * lds_f(pw_a + 4 * abs(ii - 32 * b - q - x));
+              } else {
+                // l^|i-j| as a power of the row's way from these 16 columns'
+                // first (back: last) one and one of the column's way
+                const float r = rf * lds_f(pw_a + 4 * abs(ii - 32 * b - q - (back ? 15 : 0)));
+#pragma unroll
+                for (int x = 0; x < 16; ++x) v[q + x] *= r * lds_f(pw_a + 4 * (80 + x));
+              }
             }
           }
+          const bool all = b != warp && n == kC;  // the block lies within the mask
+          const uint32_t m = (uint32_t)(mask >> (32 * b));
 #pragma unroll
-          for (int x = 0; x < 16; x += 8) {
+          for (int x = 0; x < 4; ++x) {
             uint32_t pk[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              pk[e] = pack_bf16(m & (1u << (x + 2 * e)) ? v[x + 2 * e] : 0.f, m & (2u << (x + 2 * e)) ? v[x + 2 * e + 1] : 0.f);
-            sts_u4(row + (((2 * b + x / 8) ^ (i & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+            for (int e = 0; e < 4; ++e) pk[e] = pack_bf16(v[8 * x + 2 * e], v[8 * x + 2 * e + 1]);
+            if (!all) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) pk[e] &= pair_mask(m, 8 * x + 2 * e);
+            }
+            sts_u4(row + (((4 * b + x) ^ (i & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
           }
         }
-        tc_fence_before();
-        mbar_arrive(sc_free);
         fence_proxy_async_smem();
         mbar_arrive(p_ready + 8 * (it & 1));
       }
@@ -522,29 +559,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           X[x] = make_float2(y[0], y[sc]);
         }
       }
-      auto publish = [&] {
+      auto publish = [&](int it) {
+        const float lx = steep ? 1.f : lds_f(tab_a + 4 * (2 * 2 * kC + 72 + 4 * set_of(chunk_at(it))));
+        const float2 sc = make_float2(lx, lx);
 #pragma unroll
         for (int b = 0; b < DP / 32; ++b) {
-          uint32_t hi[4], lo[4];
+          uint32_t y[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            float2 y = X[4 * b + x];
-            asm volatile("" : "+f"(y.x), "+f"(y.y));  // block by block: fewer registers at once
-            hi[x] = take_bf16(y);
-            lo[x] = as_u32(__floats2bfloat162_rn(y.x, y.y));
+            float2 z = X[4 * b + x];
+            asm volatile("" : "+f"(z.x), "+f"(z.y));  // piece by piece: fewer registers at once
+            z = __fmul2_rn(z, sc);
+            y[x] = as_u32(__floats2bfloat162_rn(z.x, z.y));
           }
-          tmem_st4(tmem + lanes + F::kX + part * (DP / 8) + 4 * b, hi);
-          tmem_st4(tmem + lanes + F::kX + DP / 2 + part * (DP / 8) + 4 * b, lo);
+          tmem_st4(tmem + lanes + F::kX + part * (DP / 8) + 4 * b, y);
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(x_ready);
+        mbar_arrive(qx_ok);
       };
-      if (!SUMS && nch > 0) publish();
+      for (int i = 0; i < kBufU; ++i) mbar_arrive(kv_ok + 8 * i);  // nothing in U yet
+      if (!SUMS && nch > 0) publish(0);
       bool ok = true;
       uint32_t turn = 0x80000000u;
       for (int it = 0; it < nch; ++it) {
-        const float4 ca = lds_f4(tab_a + 4 * (2 * 3 * kC + 72 + 4 * set_of(chunk_at(it))));
+        const float4 ca = lds_f4(tab_a + 4 * (2 * 2 * kC + 72 + 4 * set_of(chunk_at(it))));
         const uint32_t before = turn;
         turn += __float_as_uint(ca.z);
         const float ll = turn < before ? ca.y : ca.x;
@@ -563,12 +602,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();
-        mbar_arrive(u_free + 8 * buf(it));
+        mbar_arrive(kv_ok + 8 * buf(it + kBufU));
         if (!SUMS && it + 1 < nch) {
           ok = warp_wait(qx_done, (uint32_t)(it & 1), abort);
           if (!ok) break;
           tc_fence_after();
-          publish();
+          publish(it + 1);
         }
       }
       if (!ok) fail(abort, p.info);
@@ -607,8 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = 2 * (lane & 3);  // this lane's tokens: 8 n + tok, + 1
       auto values = [&](int it, int h, uint32_t at) {
         const int s = it % F::kStages, c = chunk_at(it), n = rows_of(c);
-        const uint32_t v = smem_a + s * F::kStageBytes + 2 * F::kTile;
-        const uint32_t wt = tab_a + set_of(c) * (3 * kC * 4) + 4 * tok;
+        const uint32_t v = smem_a + s * F::kStageBytes + F::kOffV;
+        const uint32_t wt = tab_a + set_of(c) * (2 * kC * 4) + 4 * tok;
         ok = warp_wait(full0 + 8 * s, (uint32_t)((it / F::kStages) & 1), abort);
         if (!ok) return;
         uint32_t x[16];
@@ -636,9 +675,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               l[2 * e + q] = as_u32(__floats2bfloat162_rn(y.x, y.y));
             }
           }
-          // the U of the chunk before in this buffer has read its weighted values
-          if (half == 0 && it >= kBuf) {
-            ok = warp_wait(kv_full + 8 * buf(it), phase(it - kBuf), abort);
+          // the products of the chunk before in this buffer have read it
+          if (half == 0 && it >= 2) {
+            if (SUMS)
+              ok = warp_wait(kv_full + 8 * buf(it), phase(it - 2), abort);
+            else if (!warp_test(kv_full + 8 * buf(it), phase(it - 2), pv_done + 8 * buf(it), phase(it - 2)))
+              ok = warp_wait(kv_full + 8 * buf(it), phase(it - 2), abort) &&
+                   warp_wait(pv_done + 8 * buf(it), phase(it - 2), abort);
             if (!ok) return;
             tc_fence_after();
           }
@@ -656,22 +699,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t ch = (uint32_t)(sub * 4 + h * 2 + (lane & 1));
             const uint32_t a = v + (ch >> 3) * kPanel + y * 128 + (((ch & 7) ^ (uint32_t)(y & 7)) << 4);
             sts_u4(a, 0, 0, 0, 0);
-            sts_u4(a - F::kTile, 0, 0, 0, 0);
+            sts_u4(a - F::kOffV + F::kOffK, 0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(vt_ready + 8 * buf(it));
+        mbar_arrive(kv_ok + 8 * buf(it));
       };
       auto outputs = [&](int it, uint32_t at0, uint32_t at1) {
         const int c = chunk_at(it), n = rows_of(c), t0 = w.begin + c * kC;
-        const uint32_t f = tab_a + (set_of(c) * 3 + 2) * kC * 4 + 4 * tok;
+        const uint32_t f = tab_a + (set_of(c) * 2 + 1) * kC * 4 + 4 * tok;
         // the store before the last one has read this staging tile
         const uint32_t ob = ob0 + (it & 1) * F::kTile;
         if (gt == 0) bulk_wait_read<1>();
         asm volatile("bar.sync 1, %0;" ::"n"(DP) : "memory");
-        ok = ok && warp_wait(pv_done, (uint32_t)(it & 1), abort);
+        ok = ok && warp_wait(pv_done + 8 * buf(it), phase(it), abort);
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -680,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_frag(tmem + lanes + ((uint32_t)(16 * h) << 16) + F::kO, v);
           if (h == 1) {
             tc_fence_before();
-            mbar_arrive(o_free);
+            mbar_arrive(qx_ok);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -721,6 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int it = 0; it < nch && ok; ++it) values(it, h, at);
       } else if (!SUMS) {
         const uint32_t at0 = row_at(0), at1 = row_at(1);
+        mbar_arrive(qx_ok);  // nothing in O yet
         // after a failed wait: keep the barriers, skip the work
         for (int it = 0; it < nch; ++it) outputs(it, at0, at1);
       }
@@ -754,7 +798,7 @@ bool make_token_map(CUtensorMap *m, void *base, long long BH, int N, int d) {
 
 template <int DP, bool SUMS>
 cudaError_t launch_t(const DecayMaps &maps, const DecayArgs &a, cudaStream_t st) {
-  constexpr size_t smem = Cfg<DP>::kSmem;
+  constexpr size_t smem = Cfg<DP, SUMS>::kSmem;
   static_assert(smem <= 232448, "shared memory");
   auto *kern = decay_tc_kernel<DP, SUMS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
