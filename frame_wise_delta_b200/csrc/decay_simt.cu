@@ -24,6 +24,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kC = kDecayC;
 
+// CTAs per SM, by shared memory and registers.
+constexpr int simt_ctas(int d) { return d == 128 ? 1 : d == 64 ? 2 : 3; }
+
 template <int D>
 struct SimtSmem {
   float q[kC][D + 4], k[kC][D + 4], v[kC][D + 4];
@@ -61,7 +64,7 @@ __device__ __forceinline__ void load_rows(const T *src, int rows, float (*dst)[D
 
 // SUMS: only the state that a segment adds (from zero), into the workspace.
 template <typename TI, typename TO, int D, bool SUMS>
-__global__ void __launch_bounds__(kThreads, 1) decay_simt_kernel(const DecayArgs p) {
+__global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(const DecayArgs p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SimtSmem<D> &s = *reinterpret_cast<SimtSmem<D> *>(smem_raw);
   constexpr int VW = D / 16 < 4 ? D / 16 : 4;  // value channels per vector
@@ -266,16 +269,25 @@ __global__ void __launch_bounds__(256) decay_prefix_kernel(const DecayArgs p, in
     }
   }
   float *ws = p.ws + pair * p.nseg * dd + e;
-  for (int n = 0; n <= w.last_seg; ++n) {
-    const int seg = op.back ? w.last_seg - n : n;
-    float4 *at = reinterpret_cast<float4 *>(ws + seg * dd);
-    const float4 u = n < w.last_seg ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
-    *at = make_float4((float)s[0], (float)s[1], (float)s[2], (float)s[3]);
-    const double l = seg == w.last_seg ? tail : full;
-    s[0] = fma(s[0], l, (double)u.x);
-    s[1] = fma(s[1], l, (double)u.y);
-    s[2] = fma(s[2], l, (double)u.z);
-    s[3] = fma(s[3], l, (double)u.w);
+  constexpr int kAhead = 8;  // segments in flight
+  for (int n0 = 0; n0 <= w.last_seg; n0 += kAhead) {
+    float4 u[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int n = n0 + x, seg = op.back ? w.last_seg - n : n;
+      u[x] = n < w.last_seg ? *reinterpret_cast<const float4 *>(ws + seg * dd) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int n = n0 + x, seg = op.back ? w.last_seg - n : n;
+      if (n > w.last_seg) break;
+      *reinterpret_cast<float4 *>(ws + seg * dd) = make_float4((float)s[0], (float)s[1], (float)s[2], (float)s[3]);
+      const double l = seg == w.last_seg ? tail : full;
+      s[0] = fma(s[0], l, (double)u[x].x);
+      s[1] = fma(s[1], l, (double)u[x].y);
+      s[2] = fma(s[2], l, (double)u[x].z);
+      s[3] = fma(s[3], l, (double)u[x].w);
+    }
   }
 }
 
@@ -382,18 +394,24 @@ cudaError_t launch_step_d(const void *Q, const void *K, const void *V, const flo
 
 }  // namespace
 
-DecaySplit decay_split(long long pairs, long long n) {
-  // Times in chunks of a walk: a wave of CTAs walks `len` chunks of its
+DecaySplit decay_split(long long pairs, long long n, int slots, bool ragged) {
+  // Times in halves of a chunk's: a wave of CTAs walks `len` chunks of its
   // segment after a start of kStart chunks' time; more than one segment adds
   // a pass for the states in front of the segments (half the traffic, no
-  // outputs) and their join.
-  constexpr long long kSms = 148, kStart = 4, kJoin = 6;
+  // outputs) and their join. Ragged sequences are half full on average, and
+  // the CTAs of short ones leave their place at once: then the longest walk or
+  // half of the whole work counts, whichever is more.
+  constexpr long long kStart = 4, kJoin = 6;
   const long long chunks = (n + kDecayC - 1) / kDecayC;
   long long best = 1, best_len = chunks > 0 ? chunks : 1, cost = -1;
-  for (long long want = 1; want <= chunks && want <= kSms; ++want) {
+  for (long long want = 1; want <= chunks && want <= slots; ++want) {
     const long long len = (chunks + want - 1) / want, nseg = (chunks + len - 1) / len;
-    const long long waves = (pairs * nseg + kSms - 1) / kSms;
-    const long long c = 2 * waves * (len + kStart) + (nseg > 1 ? waves * (len + 2 * kStart) + 2 * kJoin : 0);
+    auto pass = [&](long long walk) {
+      if (!ragged) return (pairs * nseg + slots - 1) / slots * walk;
+      const long long all = (pairs * nseg * walk / 2 + slots - 1) / slots;
+      return all > walk ? all : walk;
+    };
+    const long long c = 2 * pass(len + kStart) + (nseg > 1 ? pass(len + 2 * kStart) + 2 * kJoin : 0);
     if (cost < 0 || c < cost) {
       cost = c;
       best = nseg;
@@ -401,6 +419,10 @@ DecaySplit decay_split(long long pairs, long long n) {
     }
   }
   return DecaySplit{(int)best, (int)(best_len * kDecayC)};
+}
+
+int decay_slots(int in_dtype, int out_dtype, int d) {
+  return 148 * (decay_tc_supported(in_dtype, out_dtype) ? 1 : simt_ctas(d));
 }
 
 cudaError_t launch_decay_simt(const DecayArgs &a, int in_dtype, int out_dtype, bool sums, cudaStream_t st) {

@@ -59,29 +59,36 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   const int P = p.d >> 1;
   float2 *cs = reinterpret_cast<float2 *>(smem_raw);                     // [tokens][P]
   double *turn = reinterpret_cast<double *>(cs + (size_t)tokens * P);    // [P]
+  double *where = turn + P;                                              // [tokens][3]
   const int b = blockIdx.z;
   const long long n0 = (long long)blockIdx.x * tokens;
   const int nt = (int)min((long long)tokens, p.N - n0);
   const int rot = p.npairs[0] + p.npairs[1] + p.npairs[2];
 
   for (int i = threadIdx.x; i < rot; i += kThreads) turn[i] = p.turn[i];
-  __syncthreads();
-  for (int e = threadIdx.x; e < nt * rot; e += kThreads) {
-    const int t = e / rot, i = e - t * rot;
-    const int axis = i < p.npairs[0] ? 0 : i < p.npairs[0] + p.npairs[1] ? 1 : 2;
-    const long long n = n0 + t;
-    double at;
+  if ((int)threadIdx.x < nt) {
+    const long long n = n0 + threadIdx.x;
+    double *at = where + 3 * threadIdx.x;
     if (p.pos) {
-      at = (double)p.pos[((long long)b * p.N + n) * 3 + axis];
+      const int32_t *q = p.pos + ((long long)b * p.N + n) * 3;
+      at[0] = q[0], at[1] = q[1], at[2] = q[2];
     } else {
-      const long long f = n / p.U;
-      const int u = (int)(n - f * p.U);
-      at = axis == 0 ? (double)(p.frame0 + f) : axis == 1 ? (double)(u / p.gw) : (double)(u % p.gw);
+      const uint32_t f = (uint32_t)n / (uint32_t)p.U, u = (uint32_t)n - f * (uint32_t)p.U, row = u / (uint32_t)p.gw;
+      at[0] = (double)(p.frame0 + f), at[1] = row, at[2] = u - row * (uint32_t)p.gw;
     }
-    const double a = at * turn[i];
-    float s, c;
-    sincospif(2.f * (float)(a - rint(a)), &s, &c);
-    cs[t * P + i] = make_float2(c, p.inverse ? -s : s);
+  }
+  __syncthreads();
+  // thread: pairs i, i + step, ..; tokens t, t + kThreads / step, ..
+  const int step = P < kThreads ? P : kThreads;  // P is a power of two
+  for (int i = threadIdx.x & (step - 1); i < rot; i += step) {
+    const int axis = i < p.npairs[0] ? 0 : i < p.npairs[0] + p.npairs[1] ? 1 : 2;
+    const double per = turn[i];
+    for (int t = threadIdx.x / step; t < nt; t += kThreads / step) {
+      const double a = where[3 * t + axis] * per;
+      float s, c;
+      sincospif(2.f * (float)(a - rint(a)), &s, &c);
+      cs[t * P + i] = make_float2(c, p.inverse ? -s : s);
+    }
   }
   __syncthreads();
 
@@ -105,14 +112,19 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     float2 w[PW];
 #pragma unroll
     for (int x = 0; x < PW; ++x) w[x] = i + x < rot ? cs[t * P + i + x] : make_float2(1.f, 0.f);
-#pragma unroll 4
-    for (int sl = s0; sl < s1; ++sl) {
-      const int k = sl / p.H, h = sl - k * p.H;
+    // the slices of one tensor at a time: head by head along its stride
+    for (int sl = s0; sl < s1;) {
+      const int k = sl / p.H, h0 = sl - k * p.H, h1 = min(p.H, h0 + s1 - sl);
       const RotaryIo &io = p.io[k];
-      const T *x = (const T *)io.x + b * io.xs[0] + h * io.xs[1] + (n0 + t) * io.xs[2];
-      T *y = (T *)io.y + b * io.ys[0] + h * io.ys[1] + (n0 + t) * io.ys[2];
+      const long long xh = io.xs[1], yh = io.ys[1];
+      const T *x = (const T *)io.x + b * io.xs[0] + h0 * xh + (n0 + t) * io.xs[2];
+      T *y = (T *)io.y + b * io.ys[0] + h0 * yh + (n0 + t) * io.ys[2];
+      const bool rotate = io.rotate != 0;
+      sl += h1 - h0;
+#pragma unroll 4
+      for (int h = h0; h < h1; ++h, x += xh, y += yh) {
       Pack<T, PW> A = load<T, PW>(x + lo), B = load<T, PW>(x + hi);
-      if (io.rotate) {
+      if (rotate) {
 #pragma unroll
         for (int q = 0; q < PW; ++q) {
           // pairs that pass through are copied, not turned by 0: 0 * inf is no number
@@ -127,6 +139,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       }
       store<T, PW>(y + lo, A);
       store<T, PW>(y + hi, B);
+      }
     }
   }
 }
@@ -135,21 +148,20 @@ template <typename T, int PW, bool INTER>
 cudaError_t launch_t(const RotaryArgs &a, cudaStream_t st) {
   // tokens per block: enough for one unit per thread, at most 32 (the angles
   // of a block are shared by all heads, so few tokens per block recompute
-  // nothing); the (tensor, head) slices are spread over blocks until the
-  // card has several blocks per SM
+  // nothing); the (tensor, head) slices are spread over blocks until every SM
+  // has eight blocks: shared memory stays below 24 KB
   const int P = a.d / 2, UR = P / PW;
   int tokens = (kThreads + UR - 1) / UR;
   if (tokens < 8) tokens = 8;
   if ((long long)tokens > a.N) tokens = (int)a.N;
   const long long tiles = (a.N + tokens - 1) / tokens;
   const int all = a.nio * a.H;
-  int slices = all;
-  while (slices > 1 && tiles * a.B * ((all + slices - 1) / slices) < 4 * 148) slices = (slices + 1) / 2;
+  int parts = 1;
+  while (parts < all && tiles * a.B * parts < 8 * 148) ++parts;
+  const int slices = (all + parts - 1) / parts;
   const dim3 grid((unsigned)tiles, (unsigned)((all + slices - 1) / slices), (unsigned)a.B);
-  const size_t smem = (size_t)tokens * P * sizeof(float2) + (size_t)P * sizeof(double);
+  const size_t smem = (size_t)tokens * P * sizeof(float2) + (size_t)(P + 3 * tokens) * sizeof(double);
   auto *kern = rotary_kernel<T, PW, INTER>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, smem, st>>>(a, tokens, slices);
   return cudaGetLastError();
 }

@@ -61,6 +61,10 @@ vdn_status check_grid(long long blocks) {
   return blocks > 0x7fffffffLL ? fail(VDN_ERR_UNSUPPORTED, "too many (batch, head) pairs") : VDN_OK;
 }
 
+DecaySplit split_of(const vdn_shape *s, long long n, int nops, bool ragged) {
+  return decay_split((long long)nops * s->B * s->H, n, decay_slots(s->in_dtype, s->out_dtype, s->dk), ragged);
+}
+
 void fill_args(const vdn_shape *s, long long n, int nops, const DecaySplit &split, DecayArgs *a) {
   a->BH = (long long)s->B * s->H;
   a->H = s->H;
@@ -71,6 +75,12 @@ void fill_args(const vdn_shape *s, long long n, int nops, const DecaySplit &spli
   a->seglen = split.seglen;
 }
 
+// A query knows no lengths: the larger of the two splits.
+size_t state_bytes(const vdn_shape *s, int nops, const DecaySplit &split);
+size_t query_bytes(const vdn_shape *s, long long n, int nops) {
+  const size_t a = state_bytes(s, nops, split_of(s, n, nops, false)), b = state_bytes(s, nops, split_of(s, n, nops, true));
+  return a > b ? a : b;
+}
 size_t state_bytes(const vdn_shape *s, int nops, const DecaySplit &split) {
   if (split.nseg <= 1) return 0;
   const size_t n = (size_t)nops * s->B * s->H * split.nseg * s->dk * s->dk * sizeof(float);
@@ -158,8 +168,12 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
   for (int x = 0; x < 3; ++x) {
     if (!isfinite(scales[x])) return fail(VDN_ERR_INVALID, "scale must be finite");
     a.npairs[x] = dims[x] / 2;
+    // theta^(-2 i / n): every fourth by pow, the others by a product from there
+    double near[4] = {1.0, 0.0, 0.0, 0.0}, base = 1.0;
     for (int i = 0; i < a.npairs[x]; ++i) {
-      const double f = pow(r->theta, -2.0 * i / dims[x]) * scales[x] / (2.0 * kPi);
+      if (i < 4) near[i] = pow(r->theta, -2.0 * i / dims[x]);
+      if (i % 4 == 0) base = i ? pow(r->theta, -2.0 * i / dims[x]) : 1.0;
+      const double f = base * near[i % 4] * scales[x] / (2.0 * kPi);
       if (!isfinite(f) || fabs(f) > 1e6) return fail(VDN_ERR_INVALID, "theta and scale turn a pair by more than 1e6 turns");
       a.turn[at++] = f;
     }
@@ -219,7 +233,7 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
 size_t vdn_decay_attn_workspace_bytes(const vdn_shape *s) {
   long long n;
   if (token_count(s, &n) != VDN_OK) return 0;
-  return state_bytes(s, 1, decay_split((long long)s->B * s->H, n));
+  return query_bytes(s, n, 1);
 }
 
 vdn_status vdn_decay_attn(const vdn_shape *s, const void *Q, const void *K, const void *V, const float *log_decay,
@@ -241,8 +255,8 @@ vdn_status vdn_decay_attn(const vdn_shape *s, const void *Q, const void *K, cons
   if (any && (O == Q || O == K || O == V)) return fail(VDN_ERR_INVALID, "O is an input");
   if (BH == 0) return VDN_OK;
   if (n == 0) return copy_state(s, S_in, S_out, (cudaStream_t)stream);
-  const DecaySplit split = decay_split(BH, n);
-  VDN_TRY(check_workspace(workspace, workspace_bytes, state_bytes(s, 1, split)));
+  const DecaySplit split = split_of(s, n, 1, lens != nullptr);
+  VDN_TRY(check_workspace(workspace, workspace_bytes, query_bytes(s, n, 1)));
   VDN_TRY(check_grid(BH * split.nseg));
   DecayArgs a{};
   fill_args(s, n, 1, split, &a);
@@ -261,7 +275,7 @@ vdn_status vdn_decay_attn(const vdn_shape *s, const void *Q, const void *K, cons
 size_t vdn_decay_attn_backward_workspace_bytes(const vdn_shape *s) {
   long long n;
   if (token_count(s, &n) != VDN_OK) return 0;
-  return state_bytes(s, 3, decay_split(3LL * s->B * s->H, n));
+  return query_bytes(s, n, 3);
 }
 
 vdn_status vdn_decay_attn_backward(const vdn_shape *s, const void *Q, const void *K, const void *V,
@@ -293,8 +307,8 @@ vdn_status vdn_decay_attn_backward(const vdn_shape *s, const void *Q, const void
   if (dS_in && (dS_in == S_in || dS_in == dS_out)) return fail(VDN_ERR_INVALID, "dS_in is an input");
   if (BH == 0) return VDN_OK;
   if (n == 0) return copy_state(s, dS_out, dS_in, (cudaStream_t)stream);
-  const DecaySplit split = decay_split(3 * BH, n);
-  VDN_TRY(check_workspace(workspace, workspace_bytes, state_bytes(s, 3, split)));
+  const DecaySplit split = split_of(s, n, 3, lens != nullptr);
+  VDN_TRY(check_workspace(workspace, workspace_bytes, query_bytes(s, n, 3)));
   VDN_TRY(check_grid(3 * BH * split.nseg));
   DecayArgs a{};
   fill_args(s, n, 3, split, &a);

@@ -314,21 +314,43 @@ class vdn_rotary_io(ctypes.Structure):
                 ("y_stride", ctypes.c_int64 * 3), ("rotate", ctypes.c_int32)]
 
 
-def _here(*tensors):
-    """The token-level operators' tensors: on the current device (or None)."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and not isinstance(t, int) and (not t.is_cuda or t.get_device() != dev):
-            raise VdnError(VDN_ERR_INVALID, "tensor is not on the current CUDA device")
+_IO_WORDS = ctypes.c_int64 * 27  # three vdn_rotary_io: nine words each, `rotate` in the last one's low half
 
 
-def _typed(t, dtype, shape, name):
-    """t's pointer, or None for None; an int is a raw device pointer."""
+def _bad(text):
+    raise VdnError(VDN_ERR_INVALID, text)
+
+
+def _arg(t, dtype, shape, dev, name):
+    """The pointer of a token-level operator's tensor (None for None, an int as
+    it is): contiguous, of that type and shape, on the current device."""
     if t is None or isinstance(t, int):
         return t
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise VdnError(VDN_ERR_INVALID, f"{name} is {t.dtype} {tuple(t.shape)}, not {dtype} {shape}")
-    return _ptr(t)
+    if t.dtype != dtype or t.shape != shape:
+        _bad(f"{name} is {t.dtype} {tuple(t.shape)}, not {dtype} {shape}")
+    if t.get_device() != dev or not t.is_contiguous():
+        _bad(f"{name} is not a contiguous tensor on the current CUDA device")
+    return t.data_ptr()
+
+
+def _raw(t, dev, name):
+    """As _arg, for a buffer of any type and shape: (pointer, bytes)."""
+    if t is None or isinstance(t, int):
+        return t, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        _bad(f"{name} is not a contiguous tensor on the current CUDA device")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _device():
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _on(stream, dev):
+    """The stream's handle; the current stream of the current device for None."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 def rotary(dim_t, dim_h, dim_w, grid=(0, 0), interleaved=True, inverse=False, frame0=0, theta=10000.0,
@@ -344,34 +366,40 @@ def rotary(dim_t, dim_h, dim_w, grid=(0, 0), interleaved=True, inverse=False, fr
     return r
 
 
-def _rows(t, s, name):
+def _rows(t, shape, dtype, dev, name):
     """(pointer, batch, head and token strides) of a [B, H, T, U, d] tensor."""
-    shape, st = t.shape, t.stride()
-    if tuple(shape) != (s.B, s.H, s.T, s.U, s.dk) or t.dtype != TORCH_DTYPE[s.in_dtype]:
-        raise VdnError(VDN_ERR_INVALID, f"{name} is {t.dtype} {tuple(shape)}, not the shape's")
-    if s.dk > 1 and st[4] != 1:
-        raise VdnError(VDN_ERR_INVALID, f"{name}'s channels are not contiguous")
-    if s.T > 1 and s.U > 1 and st[2] != st[3] * s.U:
-        raise VdnError(VDN_ERR_INVALID, f"{name}'s frames do not follow each other")
-    return t.data_ptr(), st[0], st[1], st[3] if s.U > 1 else st[2]
+    if t.shape != shape or t.dtype != dtype:
+        _bad(f"{name} is {t.dtype} {tuple(t.shape)}, not {dtype} {shape}")
+    sb, sh, st, su, sd = t.stride()
+    if sd != 1:
+        _bad(f"{name}'s channels are not contiguous")
+    if shape[3] == 1:
+        su = st
+    elif shape[2] > 1 and st != su * shape[3]:
+        _bad(f"{name}'s frames do not follow each other")
+    if t.get_device() != dev:
+        _bad(f"{name} is not on the current CUDA device")
+    return t.data_ptr(), sb, sh, su
 
 
 def vdn_rotary(s, r, X, Y, rotate=None, stream=None):
     """Rotates the tensors X into Y (lists of up to three [B, H, T, U, d]
     tensors, token-major views included); rotate[i] = 0 copies X[i]."""
-    if len(X) != len(Y) or (rotate is not None and len(rotate) != len(X)):
-        raise VdnError(VDN_ERR_INVALID, "X, Y and rotate have different lengths")
+    n = len(X)
+    if n != len(Y) or n > 3 or (rotate is not None and len(rotate) != n):
+        _bad("X, Y and rotate: up to three tensors each, as many")
+    dev = _device()
+    shape, dtype = (s.B, s.H, s.T, s.U, s.dk), TORCH_DTYPE[s.in_dtype]
     pos = getattr(r, "pos_tensor", None)
-    _here(*X, *Y, pos)
-    if pos is not None and tuple(pos.shape) != (s.B, s.T * s.U, 3):
-        raise VdnError(VDN_ERR_INVALID, f"pos is {tuple(pos.shape)}, not {(s.B, s.T * s.U, 3)}")
-    io = (vdn_rotary_io * max(1, len(X)))()
-    for i, (x, y) in enumerate(zip(X, Y)):
-        e = io[i]
-        e.x, *e.x_stride[:] = _rows(x, s, "X")
-        e.y, *e.y_stride[:] = _rows(y, s, "Y")
-        e.rotate = 1 if rotate is None else int(rotate[i])
-    _check(lib().vdn_rotary(_shp(s), ctypes.byref(r), ctypes.byref(io), len(X), _stream(stream)))
+    if pos is not None:
+        _arg(pos, torch.int32, (s.B, s.T * s.U, 3), dev, "pos")
+    words = []
+    for i in range(n):
+        x, xb, xh, xt = _rows(X[i], shape, dtype, dev, "X")
+        y, yb, yh, yt = _rows(Y[i], shape, dtype, dev, "Y")
+        words += (x, y, xb, xh, xt, yb, yh, yt, 1 if rotate is None else rotate[i] & 0xFFFFFFFF)
+    io = _IO_WORDS(*words)
+    _check(lib().vdn_rotary(ctypes.byref(s), ctypes.byref(r), ctypes.byref(io), n, _on(stream, dev)))
 
 
 def vdn_decay_attn_workspace_bytes(s) -> int:
@@ -382,45 +410,43 @@ def vdn_decay_attn_backward_workspace_bytes(s) -> int:
     return int(lib().vdn_decay_attn_backward_workspace_bytes(_shp(s)))
 
 
-def _bytes(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
-
-
 def vdn_decay_attn(s, Q, K, V, log_decay, lens, S_in, O, S_out, workspace, info=None, stream=None):
     """Linear attention with one decay per head over the T * U tokens (see vdn.h); lens, S_in, S_out may be None."""
-    _here(Q, K, V, log_decay, lens, S_in, O, S_out, workspace, info)
+    dev = _device()
     x, st = (s.B, s.H, s.T, s.U, s.dk), (s.B, s.H, s.dv, s.dk)
     ti, to, f = TORCH_DTYPE[s.in_dtype], TORCH_DTYPE[s.out_dtype], torch.float32
+    ws, n = _raw(workspace, dev, "workspace")
     _check(lib().vdn_decay_attn(
-        _shp(s), _typed(Q, ti, x, "Q"), _typed(K, ti, x, "K"), _typed(V, ti, x, "V"),
-        _typed(log_decay, f, (s.H,), "log_decay"), _typed(lens, torch.int32, (s.B,), "lens"), _typed(S_in, f, st, "S_in"),
-        _typed(O, to, x, "O"), _typed(S_out, f, st, "S_out"), _ptr(workspace), _bytes(workspace), _ptr(info),
-        _stream(stream)))
+        ctypes.byref(s), _arg(Q, ti, x, dev, "Q"), _arg(K, ti, x, dev, "K"), _arg(V, ti, x, dev, "V"),
+        _arg(log_decay, f, (s.H,), dev, "log_decay"), _arg(lens, torch.int32, (s.B,), dev, "lens"),
+        _arg(S_in, f, st, dev, "S_in"), _arg(O, to, x, dev, "O"), _arg(S_out, f, st, dev, "S_out"), ws, n,
+        _raw(info, dev, "info")[0], _on(stream, dev)))
 
 
 def vdn_decay_attn_backward(s, Q, K, V, log_decay, lens, S_in, dO, dS_out, dQ, dK, dV, dS_in, workspace, info=None,
                             stream=None):
     """Gradients of vdn_decay_attn (see vdn.h); lens, S_in, dS_out, dS_in may be None."""
-    _here(Q, K, V, log_decay, lens, S_in, dO, dS_out, dQ, dK, dV, dS_in, workspace, info)
+    dev = _device()
     x, st = (s.B, s.H, s.T, s.U, s.dk), (s.B, s.H, s.dv, s.dk)
     ti, f = TORCH_DTYPE[s.in_dtype], torch.float32
+    ws, n = _raw(workspace, dev, "workspace")
     _check(lib().vdn_decay_attn_backward(
-        _shp(s), _typed(Q, ti, x, "Q"), _typed(K, ti, x, "K"), _typed(V, ti, x, "V"),
-        _typed(log_decay, f, (s.H,), "log_decay"), _typed(lens, torch.int32, (s.B,), "lens"), _typed(S_in, f, st, "S_in"),
-        _typed(dO, ti, x, "dO"), _typed(dS_out, f, st, "dS_out"), _typed(dQ, ti, x, "dQ"), _typed(dK, ti, x, "dK"),
-        _typed(dV, ti, x, "dV"), _typed(dS_in, f, st, "dS_in"), _ptr(workspace), _bytes(workspace), _ptr(info),
-        _stream(stream)))
+        ctypes.byref(s), _arg(Q, ti, x, dev, "Q"), _arg(K, ti, x, dev, "K"), _arg(V, ti, x, dev, "V"),
+        _arg(log_decay, f, (s.H,), dev, "log_decay"), _arg(lens, torch.int32, (s.B,), dev, "lens"),
+        _arg(S_in, f, st, dev, "S_in"), _arg(dO, ti, x, dev, "dO"), _arg(dS_out, f, st, dev, "dS_out"),
+        _arg(dQ, ti, x, dev, "dQ"), _arg(dK, ti, x, dev, "dK"), _arg(dV, ti, x, dev, "dV"), _arg(dS_in, f, st, dev, "dS_in"),
+        ws, n, _raw(info, dev, "info")[0], _on(stream, dev)))
 
 
 def vdn_decay_step(s, Q, K, V, log_decay, active, S_in, O, S_out, stream=None):
     """One token per sequence of vdn_decay_attn (see vdn.h); Q, K, V, O [B, H, d], S_out may be S_in."""
-    _here(Q, K, V, log_decay, active, S_in, O, S_out)
+    dev = _device()
     x, st = (s.B, s.H, s.dk), (s.B, s.H, s.dv, s.dk)
     ti, to, f = TORCH_DTYPE[s.in_dtype], TORCH_DTYPE[s.out_dtype], torch.float32
     _check(lib().vdn_decay_step(
-        _shp(s), _typed(Q, ti, x, "Q"), _typed(K, ti, x, "K"), _typed(V, ti, x, "V"),
-        _typed(log_decay, f, (s.H,), "log_decay"), _typed(active, torch.int32, (s.B,), "active"),
-        _typed(S_in, f, st, "S_in"), _typed(O, to, x, "O"), _typed(S_out, f, st, "S_out"), _stream(stream)))
+        ctypes.byref(s), _arg(Q, ti, x, dev, "Q"), _arg(K, ti, x, dev, "K"), _arg(V, ti, x, dev, "V"),
+        _arg(log_decay, f, (s.H,), dev, "log_decay"), _arg(active, torch.int32, (s.B,), dev, "active"),
+        _arg(S_in, f, st, dev, "S_in"), _arg(O, to, x, dev, "O"), _arg(S_out, f, st, dev, "S_out"), _on(stream, dev)))
 
 
 def vdn_selftest_wait(info, stream=None):

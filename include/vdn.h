@@ -491,8 +491,8 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
  * sequences: it may then be NULL), 256-byte aligned.
  * Precision: float32 sums and state. With bf16 inputs and output the products
  * run on the tensor cores: the decayed values enter the state as three bf16
- * parts (2^-24 relative), the state enters the outputs as two (2^-17), and the
- * decayed scores are rounded to bf16.
+ * parts (2^-24 relative); the scores, and the copy of the state that the
+ * outputs of a chunk read, are rounded to bf16.
  */
 size_t vdn_decay_attn_workspace_bytes(const vdn_shape *s);
 vdn_status vdn_decay_attn(const vdn_shape *s, const void *Q, const void *K, const void *V,

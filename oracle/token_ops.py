@@ -63,6 +63,32 @@ def decay_scale(q, k, v, log_decay, s_in=None, back=False, z=None):
     return m, a
 
 
+def state_reads(q, k, v, log_decay, lens=None, s_in=None, back=False, chunk=64):
+    """R_i = sum_k |X_vk| |q_ik|, X the state in front of token i's chunk (on the
+    walk back: behind it) with its decay up to token i: what a relative error of
+    that state's values can make of o_i."""
+    q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
+    B, H, n, d = q.shape
+    g = np.asarray(log_decay, np.float64)
+
+    def power(e):
+        return np.where(e == 0, 1.0, np.exp(g * max(e, 1)))[:, None, None]
+
+    r = np.zeros(v.shape)
+    for b, length in enumerate(_lens(lens, B, n)):
+        x = np.zeros((H, d, d)) if s_in is None else np.array(s_in[b], np.float64)
+        starts = list(range(0, length, chunk))
+        for a in starts[::-1] if back else starts:
+            e = min(a + chunk, length)
+            for i in range(a, e):
+                f = power(e - 1 - i if back else i - a + 1)
+                r[b, :, i] = np.einsum("hvk,hk->hv", np.abs(x) * f, np.abs(q[b, :, i]))
+            x = power(e - a) * x
+            for j in range(a, e):
+                x = x + power(j - a + 1 if back else e - 1 - j) * v[b, :, j, :, None] * k[b, :, j, None, :]
+    return r
+
+
 def rotary(x, pos, dims, theta, scale=(1.0, 1.0, 1.0), interleaved=True, inverse=False):
     """x [B, H, n, d] turned at pos [B or 1, n, 3], each pair as a complex number."""
     y = np.array(x, np.float64)

@@ -5,11 +5,13 @@ everything, segments, far positions, strided tensors) and a run of them
 together.
 
 Tolerances. Half a step is u = 2^-8 (bf16) or 2^-24 (float32) of a value. A
-bf16 output is rounded once (u |o|); the decayed scores are rounded to bf16 too
-(u M_i, M_i = sum_j l^|i-j| |q_i . k_j| |v_j|); the state enters the products as
-two bf16 parts and everything else is float32, with rounded sums of at most
-d + n + 64 terms: below 2^-13 of A_i (M_i with |q|.|k|, and |S| |q|) for the
-sizes here. A float32 output is off by 2^-24 (d + 128 + n / 64) A_i at most.
+bf16 output is rounded once (u |o|). On the tensor cores the scores are rounded
+to bf16 too (u M_i, M_i = sum_j l^|i-j| |q_i . k_j| |v_j|), and so is the copy of
+the state in front of a 64-token chunk that the outputs read (u R_i, R_i the sum
+over k of that state's |X_vk| |q_ik|). The weighted values enter with two bf16
+parts of their three (2^-15) and everything else is float32, with rounded sums
+of at most d + n + 64 terms: below 2^-13 of A_i (M_i with |q|.|k|, and |S| |q|)
+for the sizes here. A float32 output is off by 2^-24 (d + 128 + n / 64) A_i at most.
 States: in float32 each product is off by 2^-23 at most and a sum of t rounded
 additions of random sign by sqrt(t) half steps, t < 600: 2e-6 of the norm."""
 import numpy as np
@@ -55,11 +57,17 @@ def _flat(t):
     return _np(t).reshape(t.shape[0], t.shape[1], -1, t.shape[-1])
 
 
-def _near(got, ref, m, a, dt, n, d):
+def _scales(q, k, v, g, lens=None, s_in=None, back=False):
+    m, a = tok.decay_scale(q, k, v, g, s_in, back)
+    return m, a, tok.state_reads(q, k, v, g, lens, s_in, back)
+
+
+def _near(got, ref, scales, dt, n, d):
     """|got - ref| within the bound, element by element, on the rows that ref has."""
     rows = np.isfinite(ref)
+    m, a, r = scales
     if dt == "bf16":
-        tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -8 * 1.01 * m + 2.0 ** -13 * a
+        tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -8 * 1.01 * (m + r) + 2.0 ** -13 * a
     else:
         tol = 2.0 ** -24 * (d + 128 + n / 64) * a + 2.0 ** -24 * np.abs(ref)
     off = np.abs(got - ref)[rows] - tol[rows]
@@ -130,8 +138,7 @@ def test_attention(case):
     ref, ref_s = tok.decay_attn(q, k, v, _np(x["g"]), lens, s0)
     keep = np.isfinite(ref)
     q, k, v = (np.where(keep, y, 0.0) for y in (q, k, v))
-    m, a = tok.decay_scale(q, k, v, _np(x["g"]), s0)
-    _near(_flat(o), ref, m, a, "f32" if do == "f32" else "bf16", T * U, d)
+    _near(_flat(o), ref, _scales(q, k, v, _np(x["g"]), lens, s0), do, T * U, d)
     _state_near(_np(s1), ref_s)
     # rows behind the end are left as they were
     assert (_flat(o)[~keep] == MARK).all()
@@ -149,8 +156,7 @@ def test_attention_decays(d, di):
     o, s1 = _attn(s, x)
     q, k, v = (_flat(x[n]) for n in "qkv")
     ref, ref_s = tok.decay_attn(q, k, v, np.array(g), None, _np(x["s"]))
-    m, a = tok.decay_scale(q, k, v, np.array(g), _np(x["s"]))
-    _near(_flat(o), ref, m, a, di, 300, d)
+    _near(_flat(o), ref, _scales(q, k, v, np.array(g), None, _np(x["s"])), di, 300, d)
     for h in range(len(g)):
         _state_near(_np(s1)[:, h], ref_s[:, h])
 
@@ -223,10 +229,10 @@ def test_backward(case):
     keep = np.isfinite(refs[0])
     q, k, v, do = (np.where(keep, y, 0.0) for y in (q, k, v, do))
     tr = lambda t: None if t is None else np.swapaxes(t, -1, -2)  # noqa: E731
-    scales = [tok.decay_scale(do, v, k, g, tr(s0)), tok.decay_scale(v, do, q, g, tr(z), back=True),
-              tok.decay_scale(k, q, do, g, z, back=True)]
-    for got, ref, (m, a) in zip(out, refs, scales):
-        _near(_flat(got), ref, m, a, dt, T * U, d)
+    scales = [_scales(do, v, k, g, lens, tr(s0)), _scales(v, do, q, g, lens, tr(z), back=True),
+              _scales(k, q, do, g, lens, z, back=True)]
+    for got, ref, sc in zip(out, refs, scales):
+        _near(_flat(got), ref, sc, dt, T * U, d)
         assert (_flat(got)[~keep] == MARK).all()
     _state_near(_np(ds), ref_s)
 
@@ -240,10 +246,11 @@ def test_backward_decays():
     s0, z = _np(x["s"]), _np(x["z"])
     *refs, ref_s = tok.decay_attn_backward(q, k, v, np.array(g), do, None, s0, z)
     tr = lambda t: np.swapaxes(t, -1, -2)  # noqa: E731
-    scales = [tok.decay_scale(do, v, k, np.array(g), tr(s0)), tok.decay_scale(v, do, q, np.array(g), tr(z), back=True),
-              tok.decay_scale(k, q, do, np.array(g), z, back=True)]
-    for got, ref, (m, a) in zip(out, refs, scales):
-        _near(_flat(got), ref, m, a, "bf16", 300, 128)
+    g = np.array(g)
+    scales = [_scales(do, v, k, g, None, tr(s0)), _scales(v, do, q, g, None, tr(z), back=True),
+              _scales(k, q, do, g, None, z, back=True)]
+    for got, ref, sc in zip(out, refs, scales):
+        _near(_flat(got), ref, sc, "bf16", 300, 128)
     for h in range(len(g)):
         assert np.linalg.norm(_np(ds)[:, h] - ref_s[:, h]) <= 2e-6 * np.linalg.norm(ref_s[:, h]) + 1e-30
 
@@ -413,9 +420,8 @@ def _serve(prompt, steps, B, H, d, dt):
     torch.cuda.synchronize()
     got = torch.cat(outs, 2)
     ref, ref_s = tok.decay_attn(_flat(q), _flat(k), _flat(v), _np(g))
-    m, a = tok.decay_scale(_flat(q), _flat(k), _flat(v), _np(g))
     for t in (whole, got):
-        _near(_flat(t), ref, m, a, dt, n, d)
+        _near(_flat(t), ref, _scales(_flat(q), _flat(k), _flat(v), _np(g)), dt, n, d)
     _state_near(_np(state), ref_s)
     _state_near(_np(end), ref_s)
 

@@ -43,6 +43,20 @@ def test_attention_is_the_decayed_sum():
     np.testing.assert_allclose(end, s1, rtol=1e-12)
 
 
+def test_state_reads_are_the_state_in_front():
+    """With one token per chunk R_i is |l X_{i-1}| |q_i|; with one chunk it is the start state's share."""
+    q, k, v, _, g, s, _ = _draw(5)
+    r = tok.state_reads(q, k, v, g, None, s, chunk=1)
+    for i in range(q.shape[2]):
+        _, x = tok.decay_attn(q[:, :, :i], k[:, :, :i], v[:, :, :i], g, None, s)
+        want = np.einsum("bhvk,bhk->bhv", np.abs(x) * np.exp(g)[None, :, None, None], np.abs(q[:, :, i]))
+        np.testing.assert_allclose(r[:, :, i], want, rtol=1e-12)
+    r = tok.state_reads(q, k, v, g, [9, 4], s, back=True)
+    want = np.einsum("bhvk,bhk->bhv", np.abs(s), np.abs(q[:, :, 3]))
+    np.testing.assert_allclose(r[1, :, 3], want[1], rtol=1e-12)
+    assert (r[1, :, 4:] == 0).all()
+
+
 @pytest.mark.parametrize("lens", [None, [9, 4], [0, 1]])
 def test_gradients_are_the_differences(lens):
     q, k, v, do, g, s, z = _draw(2)
@@ -216,11 +230,14 @@ def test_binding_checks_types_and_shapes(L):
     with pytest.raises(vdn.VdnError):
         vdn.rotary(4, 4, 4, pos=torch.zeros(1, 3))
     with pytest.raises(vdn.VdnError):
-        vdn._typed(torch.zeros(3), torch.float32, (2,), "log_decay")
-    s = _shape(T=2, U=20)
+        vdn._arg(torch.zeros(3), torch.float32, (2,), -1, "log_decay")
+    with pytest.raises(vdn.VdnError):
+        vdn._arg(torch.zeros(3), torch.float32, (3,), 0, "log_decay")  # a host tensor
+    shape = (2, 3, 2, 20, 16)
     x = torch.zeros(2, 40, 3, 3, 16, dtype=torch.bfloat16)[:, :, 1].permute(0, 2, 1, 3).unflatten(2, (2, 20))
-    assert vdn._rows(x, s, "X")[1:] == (40 * 9 * 16, 16, 9 * 16)
-    with pytest.raises(vdn.VdnError):
-        vdn._rows(x.transpose(2, 3).contiguous().transpose(2, 3), s, "X")
-    with pytest.raises(vdn.VdnError):
-        vdn._rows(x.float(), s, "X")
+    assert vdn._rows(x, shape, torch.bfloat16, -1, "X")[1:] == (40 * 9 * 16, 16, 9 * 16)
+    for bad in (x.transpose(2, 3).contiguous().transpose(2, 3), x.float(), x.transpose(0, 1)):
+        with pytest.raises(vdn.VdnError):
+            vdn._rows(bad, shape, torch.bfloat16, -1, "X")
+    # the call packs three vdn_rotary_io as words
+    assert ctypes.sizeof(vdn.vdn_rotary_io) == 9 * 8 and vdn.vdn_rotary_io.rotate.offset == 64
