@@ -48,7 +48,7 @@ struct DecaySplit {
   int nseg, seglen;
 };
 // slots: CTAs that run at a time; ragged: the sequences end anywhere within n.
-DecaySplit decay_split(long long pairs, long long n, int slots, bool ragged);
+DecaySplit decay_split(long long pairs, long long n, int slots, bool tc, bool ragged);
 int decay_slots(int in_dtype, int out_dtype, int d);
 
 // What a CTA works on: block -> (operator, b*h, segment).

@@ -25,7 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kC = kDecayC;
 
 // CTAs per SM, by shared memory and registers.
-constexpr int simt_ctas(int d) { return d == 128 ? 1 : d == 64 ? 2 : 3; }
+constexpr int simt_ctas(int d) { return d == 128 ? 1 : 2; }
 
 template <int D>
 struct SimtSmem {
@@ -49,18 +49,34 @@ __device__ __forceinline__ void lds(const float *p, float (&r)[W]) {
   }
 }
 
+// A chunk's rows on their way to shared memory: all of a thread's loads are in
+// flight before the first is used.
 template <typename T, int D>
-__device__ __forceinline__ void load_rows(const T *src, int rows, float (*dst)[D + 4]) {
-  constexpr int V = 16 / sizeof(T);
-  for (int e = threadIdx.x; e < kC * (D / V); e += kThreads) {
-    const int r = e / (D / V), c = (e % (D / V)) * V;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (r < rows) x = *reinterpret_cast<const uint4 *>(src + (long long)r * D + c);
-    const T *y = reinterpret_cast<const T *>(&x);
+struct Rows {
+  static constexpr int V = 16 / sizeof(T), kPer = D / V, N = (kC * kPer + kThreads - 1) / kThreads;
+  uint4 x[N];
+  __device__ __forceinline__ void fetch(const T *src, int rows) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) dst[r][c + i] = to_f32(y[i]);
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + i * kThreads, r = e / kPer, c = (e % kPer) * V;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows) x[i] = *reinterpret_cast<const uint4 *>(src + (long long)r * D + c);
+    }
   }
-}
+  __device__ __forceinline__ void stash(float (*dst)[D + 4]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + i * kThreads, r = e / kPer, c = (e % kPer) * V;
+      const T *y = reinterpret_cast<const T *>(&x[i]);
+      if (r < kC) {
+#pragma unroll
+        for (int q = 0; q < V; q += 4)
+          *reinterpret_cast<float4 *>(&dst[r][c + q]) =
+              make_float4(to_f32(y[q]), to_f32(y[q + 1]), to_f32(y[q + 2]), to_f32(y[q + 3]));
+      }
+    }
+  }
+};
 
 // SUMS: only the state that a segment adds (from zero), into the workspace.
 template <typename TI, typename TO, int D, bool SUMS>
@@ -93,24 +109,43 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
       tr = op.s_in_t;
     }
   }
+  // by way of shared memory, so that memory is read along its rows
+  if (src) {
+    for (int e = threadIdx.x; e < D * D; e += kThreads) {
+      const int r = e / D, c = e % D;
+      s.st[tr ? r : c][tr ? c : r] = src[e];
+    }
+  }
+  __syncthreads();
 #pragma unroll
   for (int a = 0; a < NK; ++a)
 #pragma unroll
     for (int c = 0; c < NV; ++c)
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        const int k = ty + 16 * a, v = 16 * VW * c + VW * tx + e;
-        X[a][c * VW + e] = src ? (tr ? src[k * D + v] : src[v * D + k]) : 0.f;
-      }
+      for (int e = 0; e < VW; ++e)
+        X[a][c * VW + e] = src ? s.st[ty + 16 * a][16 * VW * c + VW * tx + e] : 0.f;
 
   const long long base = w.bh * (long long)p.N;
+  // the next chunk is fetched under this one's arithmetic where registers hold it
+  constexpr bool kEarly = D <= 64;
+  Rows<TI, D> q, k, v;
+  auto fetch = [&](int it) {
+    const int t0 = w.begin + (back ? w.nch - 1 - it : it) * kC, n = min(kC, w.end - t0);
+    const long long row = (base + t0) * D;
+    if (!SUMS) q.fetch((const TI *)p.t[op.q] + row, n);
+    k.fetch((const TI *)p.t[op.k] + row, n);
+    v.fetch((const TI *)p.t[op.v] + row, n);
+  };
+  if (kEarly && w.nch > 0) fetch(0);
   for (int it = 0; it < w.nch; ++it) {
     const int c0 = back ? w.nch - 1 - it : it;
     const int t0 = w.begin + c0 * kC, n = min(kC, w.end - t0);
     const long long row = (base + t0) * D;
-    if (!SUMS) load_rows<TI, D>((const TI *)p.t[op.q] + row, n, s.q);
-    load_rows<TI, D>((const TI *)p.t[op.k] + row, n, s.k);
-    load_rows<TI, D>((const TI *)p.t[op.v] + row, n, s.v);
+    if (!kEarly) fetch(it);
+    if (!SUMS) q.stash(s.q);
+    k.stash(s.k);
+    v.stash(s.v);
+    if (kEarly && it + 1 < w.nch) fetch(it + 1);
     if (!SUMS) {
 #pragma unroll
       for (int a = 0; a < NK; ++a)
@@ -239,8 +274,9 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
 #pragma unroll
       for (int c = 0; c < NV; ++c)
 #pragma unroll
-        for (int e = 0; e < VW; ++e)
-          dst[(16 * VW * c + VW * tx + e) * D + ty + 16 * a] = X[a][c * VW + e];
+        for (int e = 0; e < VW; ++e) s.st[ty + 16 * a][16 * VW * c + VW * tx + e] = X[a][c * VW + e];
+    __syncthreads();
+    for (int e = threadIdx.x; e < D * D; e += kThreads) dst[e] = s.st[e % D][e / D];
   }
 }
 
@@ -394,14 +430,16 @@ cudaError_t launch_step_d(const void *Q, const void *K, const void *V, const flo
 
 }  // namespace
 
-DecaySplit decay_split(long long pairs, long long n, int slots, bool ragged) {
+DecaySplit decay_split(long long pairs, long long n, int slots, bool tc, bool ragged) {
   // Times in halves of a chunk's: a wave of CTAs walks `len` chunks of its
   // segment after a start of kStart chunks' time; more than one segment adds
   // a pass for the states in front of the segments (half the traffic, no
   // outputs) and their join. Ragged sequences are half full on average, and
   // the CTAs of short ones leave their place at once: then the longest walk or
   // half of the whole work counts, whichever is more.
-  constexpr long long kStart = 4, kJoin = 6;
+  // A launch and a start cost the tensor-core kernel (1.6 us a chunk) several
+  // chunks' time, the CUDA-core one (10 us) less than one.
+  const long long kStart = tc ? 6 : 1, kJoin = tc ? 20 : 1;
   const long long chunks = (n + kDecayC - 1) / kDecayC;
   long long best = 1, best_len = chunks > 0 ? chunks : 1, cost = -1;
   for (long long want = 1; want <= chunks && want <= slots; ++want) {

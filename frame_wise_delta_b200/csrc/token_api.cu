@@ -62,7 +62,8 @@ vdn_status check_grid(long long blocks) {
 }
 
 DecaySplit split_of(const vdn_shape *s, long long n, int nops, bool ragged) {
-  return decay_split((long long)nops * s->B * s->H, n, decay_slots(s->in_dtype, s->out_dtype, s->dk), ragged);
+  return decay_split((long long)nops * s->B * s->H, n, decay_slots(s->in_dtype, s->out_dtype, s->dk),
+                     decay_tc_supported(s->in_dtype, s->out_dtype), ragged);
 }
 
 void fill_args(const vdn_shape *s, long long n, int nops, const DecaySplit &split, DecayArgs *a) {
