@@ -191,7 +191,19 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t *r) 
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// 32 TMEM lanes x 8 words: lane l's row.
+// 32 TMEM lanes x 16 (8) words: lane l's row.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
   uint32_t r[8];
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -490,35 +502,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (b == skip) continue;
-          float v[32];
-          tmem_ld32(tmem + F::kSC + ((uint32_t)(warp * 32) << 16) + 32 * b, v);
-          if (b == 1 || skip == 1) {
+        for (int b = 0; b < 4; ++b) {  // 16 columns
+          if ((b >> 1) == skip) continue;
+          float v[16];
+          tmem_ld16(tmem + F::kSC + ((uint32_t)(warp * 32) << 16) + 16 * b, v);
+          if (b == 3 || (b == 1 && skip == 1)) {
             tc_fence_before();
             mbar_arrive(sc_free);
           }
           if (steep) {
             const int ii = pinned(i);
             const float rf = 1.f / lds_f(t + 4 * (kC + ii));
+            // 1: l^|i-j| as a power of the row's way from these 16 columns'
+            // first (back: last) one and one of the column's way
+            const float r = rf * lds_f(pw_a + 4 * abs(ii - 16 * b - (back ? 15 : 0)));
 #pragma unroll
-            for (int q = 0; q < 32; q += 16) {
-              if (steep == 2) {
-#pragma unroll
-                for (int x = 0; x < 16; ++x) v[q + x] *= rf * lds_f(pw_a + 4 * abs(ii - 32 * b - q - x));
-              } else {
-                // l^|i-j| as a power of the row's way from these 16 columns'
-                // first (back: last) one and one of the column's way
-                const float r = rf * lds_f(pw_a + 4 * abs(ii - 32 * b - q - (back ? 15 : 0)));
-#pragma unroll
-                for (int x = 0; x < 16; ++x) v[q + x] *= r * lds_f(pw_a + 4 * (80 + x));
-              }
+            for (int x = 0; x < 16; ++x) {
+              const int at = pinned(steep == 2 ? abs(ii - 16 * b - x) : 80 + x);
+              v[x] *= (steep == 2 ? rf : r) * lds_f(pw_a + 4 * at);
             }
           }
-          const bool all = b != warp && n == kC;  // the block lies within the mask
-          const uint32_t m = (uint32_t)(mask >> (32 * b));
+          const bool all = (b >> 1) != warp && n == kC;  // the block lies within the mask
+          const uint32_t m = (uint32_t)(mask >> (16 * b));
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+          for (int x = 0; x < 2; ++x) {
             uint32_t pk[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) pk[e] = pack_bf16(v[8 * x + 2 * e], v[8 * x + 2 * e + 1]);
@@ -526,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) pk[e] &= pair_mask(m, 8 * x + 2 * e);
             }
-            sts_u4(row + (((4 * b + x) ^ (i & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+            sts_u4(row + (((2 * b + x) ^ (i & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
           }
         }
         fence_proxy_async_smem();
