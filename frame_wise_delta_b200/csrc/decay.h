@@ -27,6 +27,7 @@ struct DecayOp {
   int q, k, v, o;
   int back;           // walk from the last token to the first
   int s_in_t;         // s_in is read transposed
+  int ws, ws_t;       // whose segment states it starts from, read transposed or not
   const float *s_in;  // [BH, d, d] or null (zero)
   float *s_out;       // [BH, d, d] or null
 };
@@ -37,36 +38,41 @@ struct DecayArgs {
   const float *g;          // [H]
   const int32_t *lens;     // [B] or null
   int32_t *info;           // or null
-  float *ws;               // [nops * BH, nseg, d, d] with nseg > 1
+  float *ws;               // [nsums * BH, nseg * nsub, d, d] with nseg > 1
   long long BH;
   int H, N, d, nops;
-  int nseg, seglen;        // segments of a sequence; seglen is a multiple of kDecayC
+  int nsums;               // the first operators: those whose segments are summed
+  int nseg, seglen;        // segments of a sequence; seglen is a multiple of nsub * kDecayC
+  int nsub;                // parts of a segment that are summed on their own
 };
 
 // The split of the sequences over CTAs.
 struct DecaySplit {
-  int nseg, seglen;
+  int nseg, seglen, nsub;
 };
-// slots: CTAs that run at a time; ragged: the sequences end anywhere within n.
-DecaySplit decay_split(long long pairs, long long n, int slots, bool tc, bool ragged);
+// pairs, sums: (operator, batch, head) pairs of the walk and of the pass for the
+// states in front of the segments; slots: CTAs that run at a time; ragged: the sequences end anywhere within n.
+DecaySplit decay_split(long long pairs, long long sums, long long n, int slots, bool tc, bool ragged);
 int decay_slots(int in_dtype, int out_dtype, int d);
 
-// What a CTA works on: block -> (operator, b*h, segment).
+// What a CTA works on: block -> (operator, b*h, segment); `sums`: a segment's part.
 struct DecayWork {
   int op, seg, h, len, begin, end, nch, last_seg;
   long long bh;
 };
-__device__ __forceinline__ DecayWork decay_work(const DecayArgs &p, long long block) {
+__device__ __forceinline__ DecayWork decay_work(const DecayArgs &p, long long block, bool sums) {
   DecayWork w;
-  w.seg = (int)(block % p.nseg);
-  const long long r = block / p.nseg;
+  const int parts = sums ? p.nseg * p.nsub : p.nseg, plen = sums ? p.seglen / p.nsub : p.seglen;
+  const int part = (int)(block % parts);
+  w.seg = sums ? part / p.nsub : part;
+  const long long r = block / parts;
   w.bh = r % p.BH;
   w.op = (int)(r / p.BH);
   w.h = (int)(w.bh % p.H);
   w.len = p.N;
   if (p.lens) w.len = min(max(p.lens[w.bh / p.H], 0), p.N);
-  w.begin = min((long long)w.seg * p.seglen, (long long)w.len);
-  w.end = min(((long long)w.seg + 1) * p.seglen, (long long)w.len);
+  w.begin = min((long long)part * plen, (long long)w.len);
+  w.end = min(((long long)part + 1) * plen, (long long)w.len);
   w.nch = (w.end - w.begin + kDecayC - 1) / kDecayC;
   w.last_seg = w.len > 0 ? (w.len - 1) / p.seglen : 0;
   return w;
@@ -82,6 +88,22 @@ __device__ __forceinline__ bool decay_before_final(const DecayWork &w, int back)
 // bits would drift by its own error each time.
 __device__ __forceinline__ double decay_pow(float g, long long n) {
   return n == 0 ? 1.0 : exp((double)g * (double)n);
+}
+
+__device__ __forceinline__ int decay_last_part(const DecayArgs &p, int len) {
+  return len > 0 ? (len - 1) / (p.seglen / p.nsub) : 0;
+}
+// Where a walk's segment finds the state in front of it.
+__device__ __forceinline__ const float *decay_start(const DecayArgs &p, const DecayOp &op, const DecayWork &w, bool &tr) {
+  const long long dd = (long long)p.d * p.d;
+  if (p.nseg > 1) {
+    tr = op.ws_t;
+    // the segment's first part on the way
+    const int part = op.back ? min(w.seg * p.nsub + p.nsub - 1, decay_last_part(p, w.len)) : w.seg * p.nsub;
+    return p.ws + ((op.ws * p.BH + w.bh) * (p.nseg * p.nsub) + part) * dd;
+  }
+  tr = op.s_in_t;
+  return op.s_in ? op.s_in + w.bh * dd : nullptr;
 }
 
 cudaError_t launch_decay_simt(const DecayArgs &a, int in_dtype, int out_dtype, bool sums, cudaStream_t st);

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
   constexpr int VW = D / 16 < 4 ? D / 16 : 4;  // value channels per vector
   constexpr int NV = D / (16 * VW);            // vectors per thread
   constexpr int NK = D / 16;                   // key channels per thread of the state
-  const DecayWork w = decay_work(p, blockIdx.x);
+  const DecayWork w = decay_work(p, blockIdx.x, SUMS);
   const DecayOp &op = p.op[w.op];
   const int back = op.back;
   if (SUMS && !decay_before_final(w, back)) return;
@@ -101,14 +101,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
   float X[NK][NV * VW];
   const float *src = nullptr;
   bool tr = false;
-  if (!SUMS) {
-    if (p.nseg > 1) {
-      src = p.ws + (blockIdx.x) * DD;
-    } else if (op.s_in) {
-      src = op.s_in + w.bh * DD;
-      tr = op.s_in_t;
-    }
-  }
+  if (!SUMS) src = decay_start(p, op, w, tr);
   // by way of shared memory, so that memory is read along its rows
   if (src) {
     for (int e = threadIdx.x; e < D * D; e += kThreads) {
@@ -280,18 +273,21 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
   }
 }
 
-// ws[seg] becomes the state in front of segment seg on the walk: it held what
-// the segment itself adds.
+// ws[part] becomes the state in front of that part on the walk: it held what
+// the part itself adds.
 __global__ void __launch_bounds__(256) decay_prefix_kernel(const DecayArgs p, int dd4) {
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long pair = i / dd4;
-  if (pair >= p.nops * p.BH) return;
+  if (pair >= p.nsums * p.BH) return;
   const int e = (int)(i % dd4) * 4;
-  const DecayWork w = decay_work(p, pair * p.nseg);
+  const DecayWork w = decay_work(p, pair * p.nseg, false);
   const DecayOp &op = p.op[w.op];
   const long long dd = (long long)dd4 * 4;
   const float g = p.g[w.h];
-  const double full = decay_pow(g, p.seglen), tail = decay_pow(g, w.len - (long long)w.last_seg * p.seglen);
+  const int plen = p.seglen / p.nsub, last = decay_last_part(p, w.len);
+  // parts to pass up to the final segment's first
+  const int count = op.back ? last - min(p.nsub - 1, last) : w.last_seg * p.nsub;
+  const double full = decay_pow(g, plen), tail = decay_pow(g, w.len - (long long)last * plen);
   double s[4] = {0.0, 0.0, 0.0, 0.0};
   if (op.s_in) {
     const float *src = op.s_in + w.bh * dd;
@@ -304,21 +300,21 @@ __global__ void __launch_bounds__(256) decay_prefix_kernel(const DecayArgs p, in
       s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
     }
   }
-  float *ws = p.ws + pair * p.nseg * dd + e;
-  constexpr int kAhead = 8;  // segments in flight
-  for (int n0 = 0; n0 <= w.last_seg; n0 += kAhead) {
+  float *ws = p.ws + pair * (p.nseg * p.nsub) * dd + e;
+  constexpr int kAhead = 8;  // parts in flight
+  for (int n0 = 0; n0 <= count; n0 += kAhead) {
     float4 u[kAhead];
 #pragma unroll
     for (int x = 0; x < kAhead; ++x) {
-      const int n = n0 + x, seg = op.back ? w.last_seg - n : n;
-      u[x] = n < w.last_seg ? *reinterpret_cast<const float4 *>(ws + seg * dd) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const int n = n0 + x, part = op.back ? last - n : n;
+      u[x] = n < count ? *reinterpret_cast<const float4 *>(ws + part * dd) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int x = 0; x < kAhead; ++x) {
-      const int n = n0 + x, seg = op.back ? w.last_seg - n : n;
-      if (n > w.last_seg) break;
-      *reinterpret_cast<float4 *>(ws + seg * dd) = make_float4((float)s[0], (float)s[1], (float)s[2], (float)s[3]);
-      const double l = seg == w.last_seg ? tail : full;
+      const int n = n0 + x, part = op.back ? last - n : n;
+      if (n > count) break;
+      *reinterpret_cast<float4 *>(ws + part * dd) = make_float4((float)s[0], (float)s[1], (float)s[2], (float)s[3]);
+      const double l = part == last ? tail : full;
       s[0] = fma(s[0], l, (double)u[x].x);
       s[1] = fma(s[1], l, (double)u[x].y);
       s[2] = fma(s[2], l, (double)u[x].z);
@@ -333,7 +329,7 @@ cudaError_t launch_simt_t(const DecayArgs &a, cudaStream_t st) {
   auto *kern = decay_simt_kernel<TI, TO, D, SUMS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(a.nops * a.BH * a.nseg), kThreads, smem, st>>>(a);
+  kern<<<(unsigned)(SUMS ? a.nsums * a.BH * a.nseg * a.nsub : a.nops * a.BH * a.nseg), kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -430,33 +426,41 @@ cudaError_t launch_step_d(const void *Q, const void *K, const void *V, const flo
 
 }  // namespace
 
-DecaySplit decay_split(long long pairs, long long n, int slots, bool tc, bool ragged) {
+DecaySplit decay_split(long long pairs, long long sums, long long n, int slots, bool tc, bool ragged) {
   // Times in halves of a chunk's: a wave of CTAs walks `len` chunks of its
   // segment after a start of kStart chunks' time; more than one segment adds
   // a pass for the states in front of the segments (half the traffic, no
-  // outputs) and their join. Ragged sequences are half full on average, and
-  // the CTAs of short ones leave their place at once: then the longest walk or
-  // half of the whole work counts, whichever is more.
+  // outputs; each segment cut into parts until the card is full) and their
+  // join. Ragged sequences are half full on average, and the CTAs of short
+  // ones leave their place at once: then the longest walk or half of the whole
+  // work counts, whichever is more.
   // A launch and a start cost the tensor-core kernel (1.6 us a chunk) several
   // chunks' time, the CUDA-core one (10 us) less than one.
   const long long kStart = tc ? 6 : 1, kJoin = tc ? 20 : 1;
-  const long long chunks = (n + kDecayC - 1) / kDecayC;
-  long long best = 1, best_len = chunks > 0 ? chunks : 1, cost = -1;
+  const long long chunks = n > 0 ? (n + kDecayC - 1) / kDecayC : 1;
+  DecaySplit best{1, (int)(chunks * kDecayC), 1};
+  long long cost = -1;
   for (long long want = 1; want <= chunks && want <= slots; ++want) {
-    const long long len = (chunks + want - 1) / want, nseg = (chunks + len - 1) / len;
-    auto pass = [&](long long walk) {
-      if (!ragged) return (pairs * nseg + slots - 1) / slots * walk;
-      const long long all = (pairs * nseg * walk / 2 + slots - 1) / slots;
+    long long len = (chunks + want - 1) / want, nsub = 1;
+    if (want > 1) {
+      nsub = slots / (sums * (want - 1));
+      nsub = nsub < 1 ? 1 : nsub > len ? len : nsub;
+      len = (len + nsub - 1) / nsub * nsub;
+    }
+    const long long nseg = (chunks + len - 1) / len;
+    auto pass = [&](long long ctas, long long walk) {
+      if (!ragged) return (ctas + slots - 1) / slots * walk;
+      const long long all = (ctas * walk / 2 + slots - 1) / slots;
       return all > walk ? all : walk;
     };
-    const long long c = 2 * pass(len + kStart) + (nseg > 1 ? pass(len + 2 * kStart) + 2 * kJoin : 0);
+    long long c = 2 * pass(pairs * nseg, len + kStart);
+    if (nseg > 1) c += pass(sums * (nseg - 1) * nsub, len / nsub + 2 * kStart) + 2 * kJoin;
     if (cost < 0 || c < cost) {
       cost = c;
-      best = nseg;
-      best_len = len;
+      best = DecaySplit{(int)nseg, (int)(len * kDecayC), (int)nsub};
     }
   }
-  return DecaySplit{(int)best, (int)(best_len * kDecayC)};
+  return best;
 }
 
 int decay_slots(int in_dtype, int out_dtype, int d) {
@@ -475,7 +479,7 @@ cudaError_t launch_decay_simt(const DecayArgs &a, int in_dtype, int out_dtype, b
 
 cudaError_t launch_decay_prefix(const DecayArgs &a, cudaStream_t st) {
   const int dd4 = a.d * a.d / 4;
-  const long long n = a.nops * a.BH * dd4;
+  const long long n = a.nsums * a.BH * dd4;
   decay_prefix_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, dd4);
   return cudaGetLastError();
 }

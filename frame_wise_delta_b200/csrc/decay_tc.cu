@@ -258,13 +258,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const DecayWork w = decay_work(p, blockIdx.x);
+  const DecayWork w = decay_work(p, blockIdx.x, SUMS);
   const DecayOp &op = p.op[w.op];
   const int back = pinned(op.back);
   const bool fin = w.seg == decay_final_seg(w, back);
   if (SUMS ? !decay_before_final(w, back) : (w.nch == 0 && !fin)) return;
   const int nch = pinned(w.nch), d = pinned(p.d);
-  const long long DD = (long long)d * d;
   const int tail = pinned(w.end - w.begin - (nch - 1) * kC);  // rows of the segment's last chunk
   const float g = p.g[w.h];
   // 0: l^64 >= 2^-90; 1: l^15 >= 2^-100; 2: steeper still
@@ -549,14 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 X[DP / 8];
       const float *src = nullptr;
       bool tr = false;
-      if (!SUMS) {
-        if (p.nseg > 1) {
-          src = p.ws + (long long)blockIdx.x * DD;
-        } else if (op.s_in) {
-          src = op.s_in + w.bh * DD;
-          tr = op.s_in_t;
-        }
-      }
+      if (!SUMS) src = decay_start(p, op, w, tr);
       const int sr = tr ? 1 : d, sc = tr ? d : 1;  // strides of a state's row and column
 #pragma unroll
       for (int x = 0; x < DP / 8; ++x) {
@@ -620,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) fail(abort, p.info);
       // where it goes is found anew: kept over the loop, it would cost registers
       const int tid = pinned((int)threadIdx.x), blk = pinned((int)blockIdx.x), r1 = tid & 127, c1 = ((tid >> 7) - 1) * (DP / 4);
-      const DecayWork w1 = decay_work(p, blk);
+      const DecayWork w1 = decay_work(p, blk, SUMS);
       const DecayOp &op1 = p.op[w1.op];
       float *dst = nullptr;
       if (SUMS)
@@ -810,7 +802,7 @@ cudaError_t launch_t(const DecayMaps &maps, const DecayArgs &a, cudaStream_t st)
   auto *kern = decay_tc_kernel<DP, SUMS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(a.nops * a.BH * a.nseg), kThreads, smem, st>>>(maps, a);
+  kern<<<(unsigned)(SUMS ? a.nsums * a.BH * a.nseg * a.nsub : a.nops * a.BH * a.nseg), kThreads, smem, st>>>(maps, a);
   return cudaGetLastError();
 }
 

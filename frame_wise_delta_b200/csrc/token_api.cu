@@ -61,31 +61,36 @@ vdn_status check_grid(long long blocks) {
   return blocks > 0x7fffffffLL ? fail(VDN_ERR_UNSUPPORTED, "too many (batch, head) pairs") : VDN_OK;
 }
 
-DecaySplit split_of(const vdn_shape *s, long long n, int nops, bool ragged) {
-  return decay_split((long long)nops * s->B * s->H, n, decay_slots(s->in_dtype, s->out_dtype, s->dk),
+DecaySplit split_of(const vdn_shape *s, long long n, int nops, int nsums, bool ragged) {
+  const long long BH = (long long)s->B * s->H;
+  return decay_split(nops * BH, nsums * BH, n, decay_slots(s->in_dtype, s->out_dtype, s->dk),
                      decay_tc_supported(s->in_dtype, s->out_dtype), ragged);
 }
 
-void fill_args(const vdn_shape *s, long long n, int nops, const DecaySplit &split, DecayArgs *a) {
+void fill_args(const vdn_shape *s, long long n, int nops, int nsums, const DecaySplit &split, DecayArgs *a) {
   a->BH = (long long)s->B * s->H;
   a->H = s->H;
   a->N = (int)n;
   a->d = s->dk;
   a->nops = nops;
+  a->nsums = nsums;
   a->nseg = split.nseg;
   a->seglen = split.seglen;
+  a->nsub = split.nsub;
 }
 
-// A query knows no lengths: the larger of the two splits.
-size_t state_bytes(const vdn_shape *s, int nops, const DecaySplit &split);
-size_t query_bytes(const vdn_shape *s, long long n, int nops) {
-  const size_t a = state_bytes(s, nops, split_of(s, n, nops, false)), b = state_bytes(s, nops, split_of(s, n, nops, true));
-  return a > b ? a : b;
-}
-size_t state_bytes(const vdn_shape *s, int nops, const DecaySplit &split) {
+// The states in front of the segments. A query knows no lengths: the larger of
+// the two splits.
+size_t state_bytes(const vdn_shape *s, int nsums, const DecaySplit &split) {
   if (split.nseg <= 1) return 0;
-  const size_t n = (size_t)nops * s->B * s->H * split.nseg * s->dk * s->dk * sizeof(float);
+  const size_t n = (size_t)nsums * s->B * s->H * split.nseg * split.nsub * s->dk * s->dk * sizeof(float);
   return (n + 255) & ~size_t(255);
+}
+size_t query_bytes(const vdn_shape *s, long long n, int nops, int nsums) {
+  if ((long long)s->B * s->H == 0) return 0;
+  const size_t a = state_bytes(s, nsums, split_of(s, n, nops, nsums, false));
+  const size_t b = state_bytes(s, nsums, split_of(s, n, nops, nsums, true));
+  return a > b ? a : b;
 }
 
 vdn_status check_workspace(const void *ws, size_t have, size_t want) {
@@ -234,7 +239,7 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
 size_t vdn_decay_attn_workspace_bytes(const vdn_shape *s) {
   long long n;
   if (token_count(s, &n) != VDN_OK) return 0;
-  return query_bytes(s, n, 1);
+  return query_bytes(s, n, 1, 1);
 }
 
 vdn_status vdn_decay_attn(const vdn_shape *s, const void *Q, const void *K, const void *V, const float *log_decay,
@@ -256,16 +261,16 @@ vdn_status vdn_decay_attn(const vdn_shape *s, const void *Q, const void *K, cons
   if (any && (O == Q || O == K || O == V)) return fail(VDN_ERR_INVALID, "O is an input");
   if (BH == 0) return VDN_OK;
   if (n == 0) return copy_state(s, S_in, S_out, (cudaStream_t)stream);
-  const DecaySplit split = split_of(s, n, 1, lens != nullptr);
-  VDN_TRY(check_workspace(workspace, workspace_bytes, query_bytes(s, n, 1)));
-  VDN_TRY(check_grid(BH * split.nseg));
+  const DecaySplit split = split_of(s, n, 1, 1, lens != nullptr);
+  VDN_TRY(check_workspace(workspace, workspace_bytes, query_bytes(s, n, 1, 1)));
+  VDN_TRY(check_grid(BH * split.nseg * split.nsub));
   DecayArgs a{};
-  fill_args(s, n, 1, split, &a);
+  fill_args(s, n, 1, 1, split, &a);
   a.t[0] = const_cast<void *>(Q);
   a.t[1] = const_cast<void *>(K);
   a.t[2] = const_cast<void *>(V);
   a.t[4] = O;
-  a.op[0] = DecayOp{0, 1, 2, 4, 0, 0, S_in, S_out};
+  a.op[0] = DecayOp{0, 1, 2, 4, 0, 0, 0, 0, S_in, S_out};
   a.g = log_decay;
   a.lens = lens;
   a.info = info;
@@ -276,7 +281,7 @@ vdn_status vdn_decay_attn(const vdn_shape *s, const void *Q, const void *K, cons
 size_t vdn_decay_attn_backward_workspace_bytes(const vdn_shape *s) {
   long long n;
   if (token_count(s, &n) != VDN_OK) return 0;
-  return query_bytes(s, n, 3);
+  return query_bytes(s, n, 3, 2);
 }
 
 vdn_status vdn_decay_attn_backward(const vdn_shape *s, const void *Q, const void *K, const void *V,
@@ -308,16 +313,16 @@ vdn_status vdn_decay_attn_backward(const vdn_shape *s, const void *Q, const void
   if (dS_in && (dS_in == S_in || dS_in == dS_out)) return fail(VDN_ERR_INVALID, "dS_in is an input");
   if (BH == 0) return VDN_OK;
   if (n == 0) return copy_state(s, dS_out, dS_in, (cudaStream_t)stream);
-  const DecaySplit split = split_of(s, n, 3, lens != nullptr);
-  VDN_TRY(check_workspace(workspace, workspace_bytes, query_bytes(s, n, 3)));
-  VDN_TRY(check_grid(3 * BH * split.nseg));
+  const DecaySplit split = split_of(s, n, 3, 2, lens != nullptr);
+  VDN_TRY(check_workspace(workspace, workspace_bytes, query_bytes(s, n, 3, 2)));
+  VDN_TRY(check_grid(3 * BH * split.nseg * split.nsub));
   DecayArgs a{};
-  fill_args(s, n, 3, split, &a);
+  fill_args(s, n, 3, 2, split, &a);
   for (int i = 0; i < 4; ++i) a.t[i] = const_cast<void *>(in[i]);
   for (int i = 0; i < 3; ++i) a.t[4 + i] = out[i];
-  a.op[0] = DecayOp{3, 2, 1, 4, 0, 1, S_in, nullptr};   // dQ
-  a.op[1] = DecayOp{2, 3, 0, 5, 1, 1, dS_out, nullptr}; // dK
-  a.op[2] = DecayOp{1, 0, 3, 6, 1, 0, dS_out, dS_in};   // dV
+  a.op[0] = DecayOp{3, 2, 1, 4, 0, 1, 0, 0, S_in, nullptr};    // dQ
+  a.op[1] = DecayOp{1, 0, 3, 6, 1, 0, 1, 0, dS_out, dS_in};    // dV
+  a.op[2] = DecayOp{2, 3, 0, 5, 1, 1, 1, 1, dS_out, nullptr};  // dK: the transposed states of dV's walk
   a.g = log_decay;
   a.lens = lens;
   a.info = info;
