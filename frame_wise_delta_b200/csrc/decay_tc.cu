@@ -272,24 +272,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto chunk_at = [&](int it) { return back ? nch - 1 - it : it; };
   auto rows_of = [&](int c) { return c == nch - 1 ? tail : kC; };
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < F::kStages; ++s) {
-      mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, SUMS ? 1 : 2);
+  const int loads = (SUMS ? 3 : 2);  // the warp that loads
+  const CUtensorMap *mq = &maps.m[op.q], *mk = &maps.m[op.k], *mv = &maps.m[op.v];
+  auto load = [&](int it) {
+    const uint32_t dst = smem_a + (it % F::kStages) * F::kStageBytes, fb = full0 + 8 * (it % F::kStages);
+    const int t0 = w.begin + chunk_at(it) * kC;
+    if (elect_one()) {
+      mbar_arrive_expect_tx(fb, F::kStageBytes);
+#pragma unroll
+      for (int x = 0; x < F::kPanels; ++x) {
+        if (!SUMS) tma_load_3d(dst + x * kPanel, mq, fb, 64 * x, t0, (int)w.bh);
+        tma_load_3d(dst + F::kOffK + x * kPanel, mk, fb, 64 * x, t0, (int)w.bh);
+        tma_load_3d(dst + F::kOffV + x * kPanel, mv, fb, 64 * x, t0, (int)w.bh);
+      }
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(p_ready + 8 * i, 64);
-      mbar_init(kv_ok + 8 * i, 6 * DP);  // the values are there, U has been read
-      mbar_init(kv_full + 8 * i, 1);
-      mbar_init(pv_done + 8 * i, 1);
+    __syncwarp();
+  };
+  // it sets up the barriers and starts on the first tiles before anything else
+  if (warp == loads) {
+    if (lane == 0) {
+      for (int s = 0; s < F::kStages; ++s) {
+        mbar_init(full0 + 8 * s, 1);
+        mbar_init(empty0 + 8 * s, SUMS ? 1 : 2);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(p_ready + 8 * i, 64);
+        mbar_init(kv_ok + 8 * i, 6 * DP);  // the values are there, U has been read
+        mbar_init(kv_full + 8 * i, 1);
+        mbar_init(pv_done + 8 * i, 1);
+      }
+      mbar_init(sc_full, 1);
+      mbar_init(sc_free, 64);
+      mbar_init(qx_ok, 5 * DP);  // the state is there, O has been read
+      mbar_init(qx_done, 1);
+      mbar_init(drain, 2);
+      *abort = 0;
+      fence_barrier_init();
     }
-    mbar_init(sc_full, 1);
-    mbar_init(sc_free, 64);
-    mbar_init(qx_ok, 5 * DP);  // the state is there, O has been read
-    mbar_init(qx_done, 1);
-    mbar_init(drain, 2);
-    *abort = 0;
-    fence_barrier_init();
+    __syncwarp();
+    for (int it = 0; it < nch && it < F::kStages; ++it) load(it);
   }
   if (warp == 3) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   // the weights of whole chunks (set 0) and of the segment's last one (set 1)
@@ -350,30 +371,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto turn_of = [&](int it) { return (uint32_t)((it / F::kStages) & 1); };
     auto vt_of = [&](int it) { return tm + (SUMS ? F::kVT2 : F::kVT) + (uint32_t)(it & 1) * F::kVTCols; };
     bool ok = true;
-    const CUtensorMap *mq = &maps.m[op.q], *mk = &maps.m[op.k], *mv = &maps.m[op.v];
-    auto load = [&](int it) {
-      const uint32_t dst = smem_a + (it % F::kStages) * F::kStageBytes, fb = full(it);
-      const int t0 = w.begin + chunk_at(it) * kC;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(fb, F::kStageBytes);
-#pragma unroll
-        for (int x = 0; x < F::kPanels; ++x) {
-          if (!SUMS) tma_load_3d(dst + x * kPanel, mq, fb, 64 * x, t0, (int)w.bh);
-          tma_load_3d(dst + F::kOffK + x * kPanel, mk, fb, 64 * x, t0, (int)w.bh);
-          tma_load_3d(dst + F::kOffV + x * kPanel, mv, fb, 64 * x, t0, (int)w.bh);
-        }
-      }
-      __syncwarp();
-    };
     // every copy issued lands before the CTA may leave
     auto land = [&](int loaded) {
       volatile int never = 0;
       for (int i = loaded > F::kStages ? loaded - F::kStages : 0; i < loaded; ++i) warp_wait(full(i), turn_of(i), &never);
     };
     if (warp == 2) {
-      int loaded = 0;
-      if (!SUMS)
-        for (; loaded < nch && loaded < F::kStages; ++loaded) load(loaded);
+      int loaded = min(nch, F::kStages);
       for (int it = 0; it < nch; ++it) {
         // U = (w v)^T K, the smallest parts first (the values' warps have seen the tile arrive)
         ok = warp_wait(kv_ok + 8 * buf(it), phase(it), abort);
@@ -401,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) fail(abort, p.info);
       if (!SUMS) land(loaded);
     } else if (SUMS) {
-      int loaded = 0;
+      int loaded = min(nch, F::kStages);
       for (; loaded < nch && ok; ++loaded) {
-        if (loaded >= F::kStages) ok = warp_wait(empty(loaded), turn_of(loaded - F::kStages), abort);
+        ok = warp_wait(empty(loaded), turn_of(loaded - F::kStages), abort);
         if (!ok) break;
         load(loaded);
       }
