@@ -106,6 +106,28 @@ __device__ __forceinline__ const float *decay_start(const DecayArgs &p, const De
   return op.s_in ? op.s_in + w.bh * dd : nullptr;
 }
 
+// The passes of one call overlap at their ends: a launch with `early` starts
+// while the kernel before it still runs (once every block of that one has
+// called launch_dependents or left), and waits for its results where it first
+// reads them. Before that it only reads what was there before the call.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launches() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), long long grid, int threads, size_t smem, cudaStream_t st, bool early,
+                         const A &...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 cudaError_t launch_decay_simt(const DecayArgs &a, int in_dtype, int out_dtype, bool sums, cudaStream_t st);
 // bf16 in and out: the tensor cores.
 bool decay_tc_supported(int in_dtype, int out_dtype);

@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
   const DecayWork w = decay_work(p, blockIdx.x, SUMS);
   const DecayOp &op = p.op[w.op];
   const int back = op.back;
+  launch_dependents();
   if (SUMS && !decay_before_final(w, back)) return;
   const bool fin = w.seg == decay_final_seg(w, back);
   if (!SUMS && w.nch == 0 && !fin) return;
@@ -103,6 +104,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
   bool tr = false;
   if (!SUMS) src = decay_start(p, op, w, tr);
   // by way of shared memory, so that memory is read along its rows
+  if (!SUMS) wait_for_launches();
   if (src) {
     for (int e = threadIdx.x; e < D * D; e += kThreads) {
       const int r = e / D, c = e % D;
@@ -278,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
 __global__ void __launch_bounds__(256) decay_prefix_kernel(const DecayArgs p, int dd4) {
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long pair = i / dd4;
+  launch_dependents();
   if (pair >= p.nsums * p.BH) return;
   const int e = (int)(i % dd4) * 4;
   const DecayWork w = decay_work(p, pair * p.nseg, false);
@@ -288,6 +291,7 @@ __global__ void __launch_bounds__(256) decay_prefix_kernel(const DecayArgs p, in
   // parts to pass up to the final segment's first
   const int count = op.back ? last - min(p.nsub - 1, last) : w.last_seg * p.nsub;
   const double full = decay_pow(g, plen), tail = decay_pow(g, w.len - (long long)last * plen);
+  wait_for_launches();
   double s[4] = {0.0, 0.0, 0.0, 0.0};
   if (op.s_in) {
     const float *src = op.s_in + w.bh * dd;
@@ -329,8 +333,8 @@ cudaError_t launch_simt_t(const DecayArgs &a, cudaStream_t st) {
   auto *kern = decay_simt_kernel<TI, TO, D, SUMS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(SUMS ? a.nsums * a.BH * a.nseg * a.nsub : a.nops * a.BH * a.nseg), kThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  const long long grid = SUMS ? a.nsums * a.BH * a.nseg * a.nsub : a.nops * a.BH * a.nseg;
+  return launch_after(kern, grid, kThreads, smem, st, !SUMS && a.nseg > 1, a);
 }
 
 template <typename TI, typename TO, bool SUMS>
@@ -436,28 +440,31 @@ DecaySplit decay_split(long long pairs, long long sums, long long n, int slots, 
   // work counts, whichever is more.
   // A launch and a start cost the tensor-core kernel (1.6 us a chunk) several
   // chunks' time, the CUDA-core one (10 us) less than one.
-  const long long kStart = tc ? 6 : 1, kJoin = tc ? 20 : 1;
   const long long chunks = n > 0 ? (n + kDecayC - 1) / kDecayC : 1;
   DecaySplit best{1, (int)(chunks * kDecayC), 1};
+  if (pairs > 8LL * slots) return best;  // several waves of whole walks
+  const int kStart = tc ? 6 : 1, kJoin = tc ? 20 : 1, ch = (int)chunks, np = (int)pairs, ns = (int)sums;
+  // four waves of CTAs at most
+  const int most = ch < 4 * slots / np + 1 ? ch : 4 * slots / np + 1;
   long long cost = -1;
-  for (long long want = 1; want <= chunks && want <= slots; ++want) {
-    long long len = (chunks + want - 1) / want, nsub = 1;
+  for (int want = 1; want <= most; ++want) {
+    int len = (ch + want - 1) / want, nsub = 1;
     if (want > 1) {
-      nsub = slots / (sums * (want - 1));
+      nsub = slots / (ns * (want - 1));
       nsub = nsub < 1 ? 1 : nsub > len ? len : nsub;
       len = (len + nsub - 1) / nsub * nsub;
     }
-    const long long nseg = (chunks + len - 1) / len;
-    auto pass = [&](long long ctas, long long walk) {
-      if (!ragged) return (ctas + slots - 1) / slots * walk;
-      const long long all = (ctas * walk / 2 + slots - 1) / slots;
-      return all > walk ? all : walk;
+    const int nseg = (ch + len - 1) / len;
+    auto pass = [&](int ctas, int walk) {
+      if (!ragged) return (long long)((ctas + slots - 1) / slots) * walk;
+      const long long all = ((long long)ctas * walk / 2 + slots - 1) / slots;
+      return all > walk ? all : (long long)walk;
     };
-    long long c = 2 * pass(pairs * nseg, len + kStart);
-    if (nseg > 1) c += pass(sums * (nseg - 1) * nsub, len / nsub + 2 * kStart) + 2 * kJoin;
+    long long c = 2 * pass(np * nseg, len + kStart);
+    if (nseg > 1) c += pass(ns * (nseg - 1) * nsub, len / nsub + 2 * kStart) + 2 * kJoin;
     if (cost < 0 || c < cost) {
       cost = c;
-      best = DecaySplit{(int)nseg, (int)(len * kDecayC), (int)nsub};
+      best = DecaySplit{nseg, len * kDecayC, nsub};
     }
   }
   return best;
@@ -480,8 +487,7 @@ cudaError_t launch_decay_simt(const DecayArgs &a, int in_dtype, int out_dtype, b
 cudaError_t launch_decay_prefix(const DecayArgs &a, cudaStream_t st) {
   const int dd4 = a.d * a.d / 4;
   const long long n = a.nsums * a.BH * dd4;
-  decay_prefix_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, dd4);
-  return cudaGetLastError();
+  return launch_after(decay_prefix_kernel, (n + 255) / 256, 256, 0, st, true, a, dd4);
 }
 
 cudaError_t launch_decay_step(const void *Q, const void *K, const void *V, const float *g, const int32_t *active,

@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const DecayOp &op = p.op[w.op];
   const int back = pinned(op.back);
   const bool fin = w.seg == decay_final_seg(w, back);
+  launch_dependents();
   if (SUMS ? !decay_before_final(w, back) : (w.nch == 0 && !fin)) return;
   const int nch = pinned(w.nch), d = pinned(p.d);
   const int tail = pinned(w.end - w.begin - (nch - 1) * kC);  // rows of the segment's last chunk
@@ -552,7 +553,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 X[DP / 8];
       const float *src = nullptr;
       bool tr = false;
-      if (!SUMS) src = decay_start(p, op, w, tr);
+      if (!SUMS) {
+        src = decay_start(p, op, w, tr);
+        wait_for_launches();
+      }
       const int sr = tr ? 1 : d, sc = tr ? d : 1;  // strides of a state's row and column
 #pragma unroll
       for (int x = 0; x < DP / 8; ++x) {
@@ -806,8 +810,8 @@ cudaError_t launch_t(const DecayMaps &maps, const DecayArgs &a, cudaStream_t st)
   auto *kern = decay_tc_kernel<DP, SUMS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(SUMS ? a.nsums * a.BH * a.nseg * a.nsub : a.nops * a.BH * a.nseg), kThreads, smem, st>>>(maps, a);
-  return cudaGetLastError();
+  const long long grid = SUMS ? a.nsums * a.BH * a.nseg * a.nsub : a.nops * a.BH * a.nseg;
+  return launch_after(kern, grid, kThreads, smem, st, !SUMS && a.nseg > 1, maps, a);
 }
 
 }  // namespace

@@ -54,7 +54,7 @@ __device__ __forceinline__ void store(T *p, const Pack<T, W> &x) {
 // One unit: PW pairs, either 2 PW neighbouring channels or PW channels of each
 // half. P: pairs per head (d / 2), the last `rest` of them pass through.
 template <typename T, int PW, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs p, int tokens, int slices) {
+__global__ void __launch_bounds__(kThreads, PW == 1 || INTER ? 4 : 3) rotary_kernel(const __grid_constant__ RotaryArgs p, int tokens, int slices) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const int P = p.d >> 1;
   float2 *cs = reinterpret_cast<float2 *>(smem_raw);                     // [tokens][P]
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   __syncthreads();
 
   // units of a row, then rows (tokens), then slices (tensor, head)
+  constexpr int kAhead = sizeof(T) * PW >= 16 ? 2 : 4;
   const int UR = P / PW;
   const int per = nt * UR;
   const int s0 = blockIdx.y * slices, s1 = min(s0 + slices, p.nio * p.H);
@@ -121,24 +122,35 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       T *y = (T *)io.y + b * io.ys[0] + h0 * yh + (n0 + t) * io.ys[2];
       const bool rotate = io.rotate != 0;
       sl += h1 - h0;
-#pragma unroll 4
-      for (int h = h0; h < h1; ++h, x += xh, y += yh) {
-      Pack<T, PW> A = load<T, PW>(x + lo), B = load<T, PW>(x + hi);
-      if (rotate) {
+      // kAhead heads' loads are in flight before the first store (rows do not
+      // overlap, which the compiler cannot know)
+      for (int h = h0; h < h1; h += kAhead, x += kAhead * xh, y += kAhead * yh) {
+        Pack<T, PW> A[kAhead], B[kAhead];
 #pragma unroll
-        for (int q = 0; q < PW; ++q) {
-          // pairs that pass through are copied, not turned by 0: 0 * inf is no number
-          if (i + q < rot) {
-            T &ra = INTER ? (2 * q < PW ? A.v[(2 * q) % PW] : B.v[(2 * q) % PW]) : A.v[q];
-            T &rb = INTER ? (2 * q + 1 < PW ? A.v[(2 * q + 1) % PW] : B.v[(2 * q + 1) % PW]) : B.v[q];
-            const float fa = to_f32(ra), fb = to_f32(rb);
-            store_val(&ra, fa * w[q].x - fb * w[q].y);
-            store_val(&rb, fa * w[q].y + fb * w[q].x);
+        for (int g = 0; g < kAhead; ++g)
+          if (h + g < h1) {
+            A[g] = load<T, PW>(x + g * xh + lo);
+            B[g] = load<T, PW>(x + g * xh + hi);
           }
+#pragma unroll
+        for (int g = 0; g < kAhead; ++g) {
+          if (h + g >= h1) break;
+          if (rotate) {
+#pragma unroll
+            for (int q = 0; q < PW; ++q) {
+              // pairs that pass through are copied, not turned by 0: 0 * inf is no number
+              if (i + q < rot) {
+                T &ra = INTER ? (2 * q < PW ? A[g].v[(2 * q) % PW] : B[g].v[(2 * q) % PW]) : A[g].v[q];
+                T &rb = INTER ? (2 * q + 1 < PW ? A[g].v[(2 * q + 1) % PW] : B[g].v[(2 * q + 1) % PW]) : B[g].v[q];
+                const float fa = to_f32(ra), fb = to_f32(rb);
+                store_val(&ra, fa * w[q].x - fb * w[q].y);
+                store_val(&rb, fa * w[q].y + fb * w[q].x);
+              }
+            }
+          }
+          store<T, PW>(y + g * yh + lo, A[g]);
+          store<T, PW>(y + g * yh + hi, B[g]);
         }
-      }
-      store<T, PW>(y + lo, A);
-      store<T, PW>(y + hi, B);
       }
     }
   }
@@ -148,8 +160,9 @@ template <typename T, int PW, bool INTER>
 cudaError_t launch_t(const RotaryArgs &a, cudaStream_t st) {
   // tokens per block: enough for one unit per thread, at most 32 (the angles
   // of a block are shared by all heads, so few tokens per block recompute
-  // nothing); the (tensor, head) slices are spread over blocks until every SM
-  // has eight blocks: shared memory stays below 24 KB
+  // nothing); the (tensor, head) slices are spread over blocks until the card
+  // has several waves of them, as long as eight slices share a block's angles,
+  // and then until every SM has its four blocks
   const int P = a.d / 2, UR = P / PW;
   int tokens = (kThreads + UR - 1) / UR;
   if (tokens < 8) tokens = 8;
@@ -157,7 +170,8 @@ cudaError_t launch_t(const RotaryArgs &a, cudaStream_t st) {
   const long long tiles = (a.N + tokens - 1) / tokens;
   const int all = a.nio * a.H;
   int parts = 1;
-  while (parts < all && tiles * a.B * parts < 8 * 148) ++parts;
+  while (parts * 8 < all && tiles * a.B * parts < 16 * 148) ++parts;
+  while (parts < all && tiles * a.B * parts < 4 * 148) ++parts;
   const int slices = (all + parts - 1) / parts;
   const dim3 grid((unsigned)tiles, (unsigned)((all + slices - 1) / slices), (unsigned)a.B);
   const size_t smem = (size_t)tokens * P * sizeof(float2) + (size_t)(P + 3 * tokens) * sizeof(double);
