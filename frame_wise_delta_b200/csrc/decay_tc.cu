@@ -57,12 +57,12 @@ struct Cfg {
   static constexpr uint32_t kTile = kPanels * kPanel;
   static constexpr uint32_t kOffK = SUMS ? 0 : kTile, kOffV = kOffK + kTile;  // in a stage, behind Q
   static constexpr uint32_t kStageBytes = kOffV + kTile;
-  static constexpr int kStages = SUMS ? 6 : DP == 128 ? 3 : 6;
+  static constexpr int kStages = !SUMS && DP == 128 ? 4 : 6;
   // shared memory, from a 1024-byte aligned base; a 128-row operand reads
   // 8 KB past its 64-row tile, which the next tile or P covers
   static constexpr uint32_t kOffP = kStages * kStageBytes;
-  static constexpr uint32_t kOffO = kOffP + (SUMS ? 0 : 2 * kPanel);  // two P, two output tiles
-  static constexpr uint32_t kOffTab = kOffO + (SUMS ? 0 : 2 * kTile);
+  static constexpr uint32_t kOffO = kOffP + (SUMS ? 0 : 2 * kPanel);  // two P, an output tile
+  static constexpr uint32_t kOffTab = kOffO + (SUMS ? 0 : kTile);
   static constexpr uint32_t kTabFloats = 2 * 2 * kC + 72 + 8 + 16;  // w, f per set; l^n; carries; l^-n
   static constexpr uint32_t kOffBar = kOffTab + 4 * kTabFloats;
   static constexpr uint32_t kBars = 2 * kStages + 14;
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (sub * 32 < DP) {
       bool ok = true;
       const int gt = (int)threadIdx.x - 896;  // thread of the outputs' warps
-      const uint32_t ob0 = smem_a + F::kOffO, lanes = (uint32_t)(sub * 32) << 16;
+      const uint32_t ob = smem_a + F::kOffO, lanes = (uint32_t)(sub * 32) << 16;
       // this lane's matrix row: token 8 (lane / 16) + lane % 8 of a pair of
       // token groups, channels 8 ((lane / 8) % 2) .. of a group of 16
       auto row_at = [&](int h) {
@@ -717,9 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto outputs = [&](int it, uint32_t at0, uint32_t at1) {
         const int c = chunk_at(it), n = rows_of(c), t0 = w.begin + c * kC;
         const uint32_t f = tab_a + (set_of(c) * 2 + 1) * kC * 4 + 4 * tok;
-        // the store before the last one has read this staging tile
-        const uint32_t ob = ob0 + (it & 1) * F::kTile;
-        if (gt == 0) bulk_wait_read<1>();
+        // the last store has read the staging tile
+        if (gt == 0) bulk_wait_read<0>();
         asm volatile("bar.sync 1, %0;" ::"n"(DP) : "memory");
         ok = ok && warp_wait(pv_done + 8 * buf(it), phase(it), abort);
         tc_fence_after();
