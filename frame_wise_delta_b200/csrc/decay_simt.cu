@@ -355,63 +355,54 @@ cudaError_t launch_simt_d(const DecayArgs &a, cudaStream_t st) {
 // warp covers full 128-byte lines; the row's product with q is summed over its
 // lanes by shuffles.
 constexpr int kStepThreads = 128;
-template <typename TI, typename TO, int D, int ITER>
+template <typename TI, typename TO, int D>
 __global__ void __launch_bounds__(kStepThreads)
     decay_step_kernel(const TI *Q, const TI *K, const TI *V, const float *g, const int32_t *active, const float *s_in,
                       TO *O, float *s_out, long long rows, int H) {
   constexpr int kLanes = D / 4 < 8 ? D / 4 : 8;  // lanes per row
   constexpr int NV = D / (4 * kLanes);           // 16-byte vectors per lane
-  constexpr int RW = 32 / kLanes;                // rows per warp and iteration
+  constexpr int RW = 32 / kLanes;                // rows per warp
   const int lane = threadIdx.x & 31, sub = lane % kLanes;
-  const long long first = ((long long)blockIdx.x * (kStepThreads / 32) + (threadIdx.x >> 5)) * (RW * ITER) + lane / kLanes;
-  float4 s[ITER][NV];
+  const long long row = ((long long)blockIdx.x * (kStepThreads / 32) + (threadIdx.x >> 5)) * RW + lane / kLanes;
+  const bool there = row < rows;
+  float4 s[NV];
 #pragma unroll
-  for (int it = 0; it < ITER; ++it) {
-    const long long row = first + it * RW;
-    if (row < rows) {
+  for (int c = 0; c < NV; ++c)
+    if (there) s[c] = *reinterpret_cast<const float4 *>(s_in + row * D + 4 * (sub + kLanes * c));
+  const long long bh = (there ? row : 0) / D;
+  const bool on = there && (!active || active[bh / H] != 0);
+  float acc = 0.f;
+  if (on) {
+    const double l = exp((double)g[bh % H]);
+    const float l0 = (float)l, l1 = (float)(l - (double)l0);
+    const float v = to_f32(V[row]);
 #pragma unroll
-      for (int c = 0; c < NV; ++c) s[it][c] = *reinterpret_cast<const float4 *>(s_in + row * D + 4 * (sub + kLanes * c));
-    }
-  }
+    for (int c = 0; c < NV; ++c) {
+      const long long at = bh * D + 4 * (sub + kLanes * c);
+      float *x = reinterpret_cast<float *>(&s[c]);
 #pragma unroll
-  for (int it = 0; it < ITER; ++it) {
-    const long long row = first + it * RW;
-    const bool there = row < rows;
-    const long long bh = (there ? row : 0) / D;
-    const bool on = there && (!active || active[bh / H] != 0);
-    float acc = 0.f;
-    if (on) {
-      const double l = exp((double)g[bh % H]);
-      const float l0 = (float)l, l1 = (float)(l - (double)l0);
-      const float v = to_f32(V[row]);
-#pragma unroll
-      for (int c = 0; c < NV; ++c) {
-        const long long at = bh * D + 4 * (sub + kLanes * c);
-        float *x = reinterpret_cast<float *>(&s[it][c]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = fmaf(x[e], l0, fmaf(x[e], l1, v * to_f32(K[at + e])));
-          acc = fmaf(x[e], to_f32(Q[at + e]), acc);
-        }
+      for (int e = 0; e < 4; ++e) {
+        x[e] = fmaf(x[e], l0, fmaf(x[e], l1, v * to_f32(K[at + e])));
+        acc = fmaf(x[e], to_f32(Q[at + e]), acc);
       }
     }
-#pragma unroll
-    for (int m = kLanes / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-    if (there && (on || s_out != s_in)) {
-#pragma unroll
-      for (int c = 0; c < NV; ++c) *reinterpret_cast<float4 *>(s_out + row * D + 4 * (sub + kLanes * c)) = s[it][c];
-    }
-    if (on && sub == 0) store_val(O + row, acc);
   }
+#pragma unroll
+  for (int m = kLanes / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+  if (there && (on || s_out != s_in)) {
+#pragma unroll
+    for (int c = 0; c < NV; ++c) *reinterpret_cast<float4 *>(s_out + row * D + 4 * (sub + kLanes * c)) = s[c];
+  }
+  if (on && sub == 0) store_val(O + row, acc);
 }
 
 template <typename TI, typename TO, int D>
 cudaError_t launch_step_t(const void *Q, const void *K, const void *V, const float *g, const int32_t *active,
                           const float *s_in, void *O, float *s_out, long long BH, int H, cudaStream_t st) {
   constexpr int kLanes = D / 4 < 8 ? D / 4 : 8;
-  constexpr int kRows = (32 / kLanes) * (kStepThreads / 32);  // rows per CTA and iteration
+  constexpr int kRows = (32 / kLanes) * (kStepThreads / 32);  // rows per CTA
   const long long rows = BH * D, grid = (rows + kRows - 1) / kRows;
-  decay_step_kernel<TI, TO, D, 1><<<(unsigned)grid, kStepThreads, 0, st>>>(
+  decay_step_kernel<TI, TO, D><<<(unsigned)grid, kStepThreads, 0, st>>>(
       (const TI *)Q, (const TI *)K, (const TI *)V, g, active, s_in, (TO *)O, s_out, rows, H);
   return cudaGetLastError();
 }

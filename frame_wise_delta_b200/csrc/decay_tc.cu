@@ -8,7 +8,8 @@
 //   o_i = 1/w_i (l^n X q_i + sum_j s_ij w_j v_j),   j <= i (back: j >= i),
 // since l^{i-j} = w_j / w_i and l^{i+1} = l^n / w_i (back: l^{j-i}, l^{n-1-i}). So the weighted values
 // serve both sums, the scores need no weights of their own, and both terms of o_i share one accumulator.
-// 1/w_i is at most 1/l^64. A head that decays by more than 2^-90 over a chunk ("steep") would lose its
+// 1/w_i is at most 1/l^64; values and state carry a factor 2^c, c two thirds of that range (60 at most), so
+// that values down to 1e-20 keep all of their bits under the smallest weight. A head that decays by more than 2^-90 over a chunk ("steep") would lose its
 // early values to float32's range: it takes o_i = f_i (X q_i + sum_j c_ij s_ij v_j) with f_i = max(l^{i+1}, 2^-60)
 // (back: l^{n-1-i}) and c_ij = l^{|i-j|} / f_i put on the scores; where f_i is cut off the state enters
 // with 2^-60 in place of something smaller, far below a rounding of o_i.
@@ -63,7 +64,7 @@ struct Cfg {
   static constexpr uint32_t kOffP = kStages * kStageBytes;
   static constexpr uint32_t kOffO = kOffP + (SUMS ? 0 : 2 * kPanel);  // two P, an output tile
   static constexpr uint32_t kOffTab = kOffO + (SUMS ? 0 : kTile);
-  static constexpr uint32_t kTabFloats = 2 * 2 * kC + 72 + 8 + 16;  // w, f per set; l^n; carries; l^-n
+  static constexpr uint32_t kTabFloats = 2 * 2 * kC + 72 + 8 + 16;  // w, f per set; l^n; carries and 2^c, 2^-c; l^-n
   static constexpr uint32_t kOffBar = kOffTab + 4 * kTabFloats;
   static constexpr uint32_t kBars = 2 * kStages + 14;
   static constexpr size_t kSmem = 1024 + kOffBar + 8 * kBars + 16;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nch = pinned(w.nch), d = pinned(p.d);
   const int tail = pinned(w.end - w.begin - (nch - 1) * kC);  // rows of the segment's last chunk
   const float g = p.g[w.h];
-  // 0: l^64 >= 2^-90; 1: l^15 >= 2^-100; 2: steeper still
+  // 0: l^64 >= 2^-90, values and state times 2^c; 1: l^15 >= 2^-100; 2: steeper still
   const int steep = pinned((double)g * kC >= -62.383246250395077 ? 0 : (double)g * 15 >= -69.3 ? 1 : 2);
   const uint32_t smem_a = (uint32_t)pinned((int)smem_u32(smem)), tab_a = smem_a + F::kOffTab;
   auto chunk_at = [&](int it) { return back ? nch - 1 - it : it; };
@@ -314,13 +315,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = 0; it < nch && it < F::kStages; ++it) load(it);
   }
   if (warp == 3) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  const int c2 = steep ? 0 : (int)((double)g * kC * -0.96179669392597561);  // 2 / (3 ln 2)
   // the weights of whole chunks (set 0) and of the segment's last one (set 1)
   if (threadIdx.x < 2 * kC) {
     const int set = threadIdx.x / kC, x = threadIdx.x % kC, n = set ? tail : kC;
     float *t = tab + set * 2 * kC;
     const double wx = decay_pow(g, back ? x + 1 : n - 1 - x);
-    t[x] = x < n ? (float)wx : 0.f;
-    t[kC + x] = x >= n ? 1.f : steep ? fmaxf((float)decay_pow(g, back ? n - 1 - x : x + 1), 0x1p-60f) : (float)(1.0 / wx);
+    t[x] = x < n ? (float)scalbn(wx, c2) : 0.f;
+    t[kC + x] = x >= n ? 1.f : steep ? fmaxf((float)decay_pow(g, back ? n - 1 - x : x + 1), 0x1p-60f) : (float)(1.0 / scalbn(wx, c2));
   } else if (threadIdx.x < 2 * kC + kC + 1) {
     pw[threadIdx.x - 2 * kC] = (float)decay_pow(g, threadIdx.x - 2 * kC);
   } else if (threadIdx.x >= 224 && threadIdx.x < 240) {
@@ -333,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const double l = decay_pow(g, set ? tail : kC);
     const float lo = __double2float_rd(l), hi = __double2float_ru(l);
     carry[4 * set] = lo;
+    carry[4 * set + 3] = (float)scalbn(1.0, set ? -c2 : c2);
     carry[4 * set + 1] = hi;
     carry[4 * set + 2] = __uint_as_float(hi > lo ? __double2uint_rn((l - lo) / ((double)hi - lo) * 4294967295.0) : 0u);
   }
@@ -558,12 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_for_launches();
       }
       const int sr = tr ? 1 : d, sc = tr ? d : 1;  // strides of a state's row and column
+      const float up = lds_f(tab_a + 4 * (2 * 2 * kC + 72 + 3));
 #pragma unroll
       for (int x = 0; x < DP / 8; ++x) {
         X[x] = make_float2(0.f, 0.f);
         if (src && r < d && c0 + 2 * x < d) {
           const float *y = src + r * sr + (c0 + 2 * x) * sc;
-          X[x] = make_float2(y[0], y[sc]);
+          X[x] = make_float2(up * y[0], up * y[sc]);
         }
       }
       auto publish = [&](int it) {
@@ -627,12 +631,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         dst = p.ws + (long long)blk * p.d * p.d;
       else if (w1.seg == decay_final_seg(w1, op1.back) && op1.s_out)
         dst = op1.s_out + w1.bh * (long long)p.d * p.d;
+      const float down = lds_f(tab_a + 4 * (2 * 2 * kC + 72 + 7));
       if (dst && r1 < p.d) {
 #pragma unroll
         for (int x = 0; x < DP / 4; x += 4)
           if (c1 + x < p.d)
             *reinterpret_cast<float4 *>(dst + r1 * p.d + c1 + x) =
-                make_float4(X[x / 2].x, X[x / 2].y, X[x / 2 + 1].x, X[x / 2 + 1].y);
+                make_float4(down * X[x / 2].x, down * X[x / 2].y, down * X[x / 2 + 1].x, down * X[x / 2 + 1].y);
       }
     }
   } else {

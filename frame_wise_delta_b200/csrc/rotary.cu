@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, PW == 1 || INTER ? 4 : 3) rotary_ker
 
 template <typename T, int PW, bool INTER>
 cudaError_t launch_t(const RotaryArgs &a, cudaStream_t st) {
-  // tokens per block: enough for one unit per thread, at most 32 (the angles
+  // tokens per block: enough for one unit per thread, 8 at least (the angles
   // of a block are shared by all heads, so few tokens per block recompute
   // nothing); the (tensor, head) slices are spread over blocks until the card
   // has several waves of them, as long as eight slices share a block's angles,

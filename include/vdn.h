@@ -488,7 +488,8 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
  * the start of its 64-token chunk on.
  * info: optional, as for vdn_frame_grams.
  * workspace: at least vdn_decay_attn_workspace_bytes(s) bytes (0 for short
- * sequences: it may then be NULL), 256-byte aligned.
+ * sequences: it may then be NULL), 256-byte aligned, its contents undefined
+ * before and after; calls that may run at the same time need one each.
  * Precision: float32 sums and state. With bf16 inputs and output the products
  * run on the tensor cores: the decayed values enter the state as three bf16
  * parts (2^-24 relative); the scores, and the copy of the state that the

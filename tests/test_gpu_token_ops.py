@@ -463,6 +463,128 @@ def test_other_stream_and_graph(n):
         assert all(torch.equal(a, b) for a, b in zip(grads, bw[0])) and torch.equal(ds, bw[1])
 
 
+def test_segments_summed_in_parts():
+    """Enough pairs for a few segments each, whose sums are cut further; both walks, ragged ends in every part."""
+    B, H, n, d = 2, 10, 1500, 64
+    lens = [1500, 1130]
+    x = _inputs(15, B, H, 1, n, d, "bf16", names="qkvo")
+    s = vdn.make_shape(B, H, 1, n, d, 0)
+    _poison(x, lens, "qkvo")
+    out, ds = _backward(s, x, lens)
+    o, s1 = _attn(s, x, lens)
+    q, k, v, do = (_flat(x[c]) for c in "qkvo")
+    g, s0, z = _np(x["g"]), _np(x["s"]), _np(x["z"])
+    ref, ref_s = tok.decay_attn(q, k, v, g, lens, s0)
+    *refs, ref_ds = tok.decay_attn_backward(q, k, v, g, do, lens, s0, z)
+    keep = np.isfinite(ref)
+    q, k, v, do = (np.where(keep, y, 0.0) for y in (q, k, v, do))
+    tr = lambda t: np.swapaxes(t, -1, -2)  # noqa: E731
+    _near(_flat(o), ref, _scales(q, k, v, g, lens, s0), "bf16", n, d)
+    for got, want, sc in zip(out, refs, [_scales(do, v, k, g, lens, tr(s0)), _scales(v, do, q, g, lens, tr(z), back=True),
+                                         _scales(k, q, do, g, lens, z, back=True)]):
+        _near(_flat(got), want, sc, "bf16", n, d)
+    _state_near(_np(s1), ref_s)
+    _state_near(_np(ds), ref_ds)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_steep_decays(d):
+    """Heads that forget within a chunk, on either side of each of the kernel's forms, forward and backward."""
+    g = [-0.974, -0.976, -1.5, -2.5, -4.0, -4.61, -4.63, -12.0]
+    x = _inputs(19, 1, len(g), 1, 150, d, "bf16", names="qkvo", g=g)
+    s = vdn.make_shape(1, len(g), 1, 150, d, 0)
+    o, s1 = _attn(s, x)
+    out, ds = _backward(s, x)
+    q, k, v, do = (_flat(x[c]) for c in "qkvo")
+    s0, z, g = _np(x["s"]), _np(x["z"]), np.array(g, np.float32).astype(np.float64)
+    ref, ref_s = tok.decay_attn(q, k, v, g, None, s0)
+    *refs, ref_ds = tok.decay_attn_backward(q, k, v, g, do, None, s0, z)
+    tr = lambda t: np.swapaxes(t, -1, -2)  # noqa: E731
+    scales = [_scales(q, k, v, g, None, s0), _scales(do, v, k, g, None, tr(s0)),
+              _scales(v, do, q, g, None, tr(z), back=True), _scales(k, q, do, g, None, z, back=True)]
+    for got, want, sc in zip([o, *out], [ref, *refs], scales):
+        _near(_flat(got), want, sc, "bf16", 150, d)
+    for h in range(len(g)):
+        _state_near(_np(s1)[:, h], ref_s[:, h])
+        _state_near(_np(ds)[:, h], ref_ds[:, h])
+
+
+@pytest.mark.parametrize("power", [-50, 40])
+@pytest.mark.parametrize("n", [100, 2500])
+def test_powers_of_two_pass_through(n, power):
+    """Values and state times a power of two: the same bits times that power (gradients are often
+    tiny), for heads whose weights span the widest range as well."""
+    g = [0.0, -0.01, -0.7, -0.97, -1.2, -6.0]
+    x = _inputs(20, 1, len(g), 1, n, 128, "bf16", g=g)
+    s = vdn.make_shape(1, len(g), 1, n, 128, 0)
+    o, s1 = _attn(s, x)
+    f = 2.0 ** power
+    o2, s2 = _attn(s, {**x, "v": x["v"] * f, "s": x["s"] * f})
+    assert torch.equal(o * f, o2) and torch.equal(s1 * f, s2)
+
+
+@pytest.mark.parametrize("di", ["bf16", "f32"])
+def test_lengths_are_clamped(di):
+    x = _inputs(16, 3, 2, 1, 100, 32, di)
+    s = vdn.make_shape(3, 2, 1, 100, 32, 0, in_dtype=di)
+    a = _attn(s, x, [100, 0, 37])
+    b = _attn(s, x, [2 ** 31 - 1, -(2 ** 31), 37])
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_rotary_reads_a_broadcast_axis():
+    x = torch.randn(1, 1, 4, 6, 32, device="cuda").expand(3, 5, 4, 6, 32)
+    s = vdn.make_shape(3, 5, 4, 6, 32, 0, in_dtype="f32")
+    r = vdn.rotary(16, 8, 8, grid=(2, 3))
+    y, z = torch.empty(3, 5, 4, 6, 32, device="cuda"), torch.empty(3, 5, 4, 6, 32, device="cuda")
+    vdn.vdn_rotary(s, r, [x], [y])
+    vdn.vdn_rotary(s, r, [x.contiguous()], [z])
+    assert torch.equal(y, z)
+    with pytest.raises(vdn.VdnError):
+        vdn.vdn_rotary(s, r, [z], [x])
+
+
+@pytest.mark.slow
+def test_offsets_beyond_32_bits():
+    """140 000 pairs of 128 tokens, 2.3e9 values a tensor: the last pair as exact as if it were alone."""
+    B, H, n, d = 1000, 140, 128, 128
+    one = _inputs(17, 1, 1, 1, n, d, "bf16")
+    big = {}
+    for c in "qkv":
+        big[c] = torch.zeros((B, H, 1, n, d), dtype=torch.bfloat16, device="cuda")
+        big[c][-1, -1] = one[c][0, 0]
+    g = torch.full((H,), float(one["g"][0]), device="cuda")
+    s, s1 = vdn.make_shape(B, H, 1, n, d, 0), vdn.make_shape(1, 1, 1, n, d, 0)
+    o = torch.full_like(big["q"], MARK)
+    vdn.vdn_decay_attn(s, big["q"], big["k"], big["v"], g, None, None, o, None, None)
+    want = torch.empty_like(one["q"])
+    vdn.vdn_decay_attn(s1, one["q"], one["k"], one["v"], one["g"], None, None, want, None, None)
+    assert torch.equal(o[-1, -1], want[0, 0])
+    assert (o[0, 0] == 0).all() and (o[B // 2, 3] == 0).all()
+    vdn.vdn_rotary(s, vdn.rotary(64, 32, 32, grid=(8, 16)), [big["v"]], [o])
+    vdn.vdn_rotary(s1, vdn.rotary(64, 32, 32, grid=(8, 16)), [one["v"]], [want])
+    assert torch.equal(o[-1, -1], want[0, 0])
+    del big, o
+    torch.cuda.empty_cache()
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces of their own on two streams do not disturb each other."""
+    xs = [_inputs(18 + i, 1, 2, 1, 2500, 128, "bf16") for i in range(2)]
+    s = vdn.make_shape(1, 2, 1, 2500, 128, 0)
+    want = [_attn(s, x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    ws = [vdn.workspace(vdn.vdn_decay_attn_workspace_bytes(s)) for _ in xs]
+    outs = [(torch.empty_like(x["q"]), torch.empty_like(x["s"])) for x in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, st, w, (o, s1) in zip(xs, streams, ws, outs):
+            vdn.vdn_decay_attn(s, x["q"], x["k"], x["v"], x["g"], None, x["s"], o, s1, w, stream=st)
+    torch.cuda.synchronize()
+    for (o, s1), (a, b) in zip(outs, want):
+        assert torch.equal(o, a) and torch.equal(s1, b)
+
+
 def test_binding_refuses_other_shapes():
     x = _inputs(14, 1, 2, 1, 20, 64, "bf16")
     s = vdn.make_shape(1, 2, 1, 20, 64, 0)
