@@ -220,20 +220,26 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
                : "memory");
 }
 // 16 TMEM lanes x 64 words: registers 4 n + 2 e + c of lane l are lane l / 4 +
-// 8 e, column 8 n + 2 (l % 4) + c.
+// 8 e, column 8 n + 2 (l % 4) + c. The values are there after tmem_ld_frag_wait.
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_frag_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                 "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                 "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -727,27 +733,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("bar.sync 1, %0;" ::"n"(DP) : "memory");
         ok = ok && warp_wait(pv_done + 8 * buf(it), phase(it), abort);
         tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!ok) break;
+        if (ok) {
+          const uint32_t o = tmem + lanes + F::kO;
           float v[32];
-          tmem_ld_frag(tmem + lanes + ((uint32_t)(16 * h) << 16) + F::kO, v);
-          if (h == 1) {
-            tc_fence_before();
-            mbar_arrive(qx_ok);
-          }
+          uint32_t y[16];
+          auto pack = [&]() {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t y[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int m = 2 * e + (q >> 1);
+            for (int m = 0; m < 8; ++m) {
               const float2 f2 = lds_f2(f + 32 * m);
-              const float2 z = __fmul2_rn(make_float2(v[4 * m + 2 * (q & 1)], v[4 * m + 2 * (q & 1) + 1]), f2);
-              y[q] = as_u32(__floats2bfloat162_rn(z.x, z.y));
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const float2 z = __fmul2_rn(make_float2(v[4 * m + 2 * q], v[4 * m + 2 * q + 1]), f2);
+                y[2 * m + q] = as_u32(__floats2bfloat162_rn(z.x, z.y));
+              }
             }
-            stsm4t(ob + (h ? at1 : at0) + e * 2048, y[0], y[1], y[2], y[3]);
-          }
+          };
+          auto stage = [&](uint32_t at) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) stsm4t(ob + at + e * 2048, y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          };
+          tmem_ld_frag(o, v);
+          tmem_ld_frag_wait(v);
+          pack();
+          tmem_ld_frag(o + (16u << 16), v);  // under the first half's way out
+          stage(at0);
+          tmem_ld_frag_wait(v);
+          tc_fence_before();
+          mbar_arrive(qx_ok);
+          pack();
+          stage(at1);
         }
         fence_proxy_async_smem();
         asm volatile("bar.sync 1, %0;" ::"n"(DP) : "memory");
