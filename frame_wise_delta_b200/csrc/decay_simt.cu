@@ -21,19 +21,20 @@
 namespace vdn {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kC = kDecayC;
 
+constexpr int kThreads = 256;
 // CTAs per SM, by shared memory and registers.
 constexpr int simt_ctas(int d) { return d == 128 ? 1 : 2; }
 
 template <int D>
 struct SimtSmem {
   float q[kC][D + 4], k[kC][D + 4], v[kC][D + 4];
-  float st[D][D + 4];  // the state, st[key][value]
+  float wk[kC][D + 4];  // the keys times their weights in the chunk's sum
+  float st[D][D + 4];   // the state, st[key][value]
   float p[kC][kC + 4];
-  float pw[kC + 1];    // l^n
-  float carry[2];      // l^n of the chunk's valid rows, as two floats
+  float pw[kC + 1];     // l^n
+  float carry[2][2];    // l^n of a whole chunk and of the segment's last one, as two floats each
 };
 
 template <int W>
@@ -47,6 +48,16 @@ __device__ __forceinline__ void lds(const float *p, float (&r)[W]) {
   } else {
     r[0] = p[0];
   }
+}
+
+template <int W>
+__device__ __forceinline__ void sts(float *p, const float *r) {
+  if constexpr (W == 4)
+    *reinterpret_cast<float4 *>(p) = make_float4(r[0], r[1], r[2], r[3]);
+  else if constexpr (W == 2)
+    *reinterpret_cast<float2 *>(p) = make_float2(r[0], r[1]);
+  else
+    p[0] = r[0];
 }
 
 // A chunk's rows on their way to shared memory: all of a thread's loads are in
@@ -63,29 +74,41 @@ struct Rows {
       if (r < rows) x[i] = *reinterpret_cast<const uint4 *>(src + (long long)r * D + c);
     }
   }
-  __device__ __forceinline__ void stash(float (*dst)[D + 4]) const {
+  // dst = the rows times weight(row)
+  template <typename W>
+  __device__ __forceinline__ void stash(float (*dst)[D + 4], W weight) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = threadIdx.x + i * kThreads, r = e / kPer, c = (e % kPer) * V;
       const T *y = reinterpret_cast<const T *>(&x[i]);
       if (r < kC) {
+        const float f = weight(r);
 #pragma unroll
         for (int q = 0; q < V; q += 4)
           *reinterpret_cast<float4 *>(&dst[r][c + q]) =
-              make_float4(to_f32(y[q]), to_f32(y[q + 1]), to_f32(y[q + 2]), to_f32(y[q + 3]));
+              make_float4(f * to_f32(y[q]), f * to_f32(y[q + 1]), f * to_f32(y[q + 2]), f * to_f32(y[q + 3]));
       }
     }
+  }
+  __device__ __forceinline__ void stash(float (*dst)[D + 4]) const {
+    stash(dst, [](int) { return 1.f; });
   }
 };
 
 // SUMS: only the state that a segment adds (from zero), into the workspace.
+// A warp is a grid of 4 x 8 threads over rows x columns of each product: its
+// 16-byte reads of either operand then touch 64 and 128 bytes of different
+// banks, one pass of the shared memory each.
 template <typename TI, typename TO, int D, bool SUMS>
 __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(const DecayArgs p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SimtSmem<D> &s = *reinterpret_cast<SimtSmem<D> *>(smem_raw);
+  constexpr int TY = kThreads / 16;            // threads over rows; 16 over columns
+  constexpr int R = kC / TY;                   // rows per thread of the scores and outputs
   constexpr int VW = D / 16 < 4 ? D / 16 : 4;  // value channels per vector
   constexpr int NV = D / (16 * VW);            // vectors per thread
-  constexpr int NK = D / 16;                   // key channels per thread of the state
+  constexpr int NK = D / TY;                   // key channels per thread of the state
+  constexpr int KW = NK < 4 ? NK : 4, NKV = NK / KW;  // in vectors
   const DecayWork w = decay_work(p, blockIdx.x, SUMS);
   const DecayOp &op = p.op[w.op];
   const int back = op.back;
@@ -93,32 +116,9 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
   if (SUMS && !decay_before_final(w, back)) return;
   const bool fin = w.seg == decay_final_seg(w, back);
   if (!SUMS && w.nch == 0 && !fin) return;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tx = (warp & 1) * 8 + (lane & 7), ty = (warp >> 1) * 4 + (lane >> 3);
   constexpr long long DD = (long long)D * D;
-  const float g = p.g[w.h];
-  if (threadIdx.x <= kC) s.pw[threadIdx.x] = (float)decay_pow(g, threadIdx.x);
-
-  // the state: this thread's key channels ty + 16 a, value channels 16 VW c + VW tx
-  float X[NK][NV * VW];
-  const float *src = nullptr;
-  bool tr = false;
-  if (!SUMS) src = decay_start(p, op, w, tr);
-  // by way of shared memory, so that memory is read along its rows
-  if (!SUMS) wait_for_launches();
-  if (src) {
-    for (int e = threadIdx.x; e < D * D; e += kThreads) {
-      const int r = e / D, c = e % D;
-      s.st[tr ? r : c][tr ? c : r] = src[e];
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int a = 0; a < NK; ++a)
-#pragma unroll
-    for (int c = 0; c < NV; ++c)
-#pragma unroll
-      for (int e = 0; e < VW; ++e)
-        X[a][c * VW + e] = src ? s.st[ty + 16 * a][16 * VW * c + VW * tx + e] : 0.f;
 
   const long long base = w.bh * (long long)p.N;
   // the next chunk is fetched under this one's arithmetic where registers hold it
@@ -132,129 +132,142 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
     v.fetch((const TI *)p.t[op.v] + row, n);
   };
   if (kEarly && w.nch > 0) fetch(0);
+
+  const float g = p.g[w.h];
+  if (threadIdx.x <= kC) {
+    s.pw[threadIdx.x] = (float)decay_pow(g, threadIdx.x);
+  } else if (threadIdx.x >= 96 && threadIdx.x < 98) {
+    const int set = threadIdx.x - 96;
+    const double l = decay_pow(g, set ? w.end - w.begin - (w.nch - 1) * kC : kC);
+    s.carry[set][0] = (float)l;
+    s.carry[set][1] = (float)(l - (double)(float)l);
+  }
+
+  // the state: this thread's key channels KW (TY a + ty) + e, value channels VW (16 c + tx) + x
+  float X[NK][NV * VW];
+  const float *src = nullptr;
+  bool tr = false;
+  if (!SUMS) {
+    src = decay_start(p, op, w, tr);
+    wait_for_launches();
+  }
+  // by way of shared memory, so that memory is read along its rows
+  if (src) {
+    for (int e = threadIdx.x; e < D * D; e += kThreads) {
+      const int r = e / D, c = e % D;
+      s.st[tr ? r : c][tr ? c : r] = src[e];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int a = 0; a < NK; ++a)
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+      for (int e = 0; e < VW; ++e)
+        X[a][c * VW + e] = src ? s.st[KW * (TY * (a / KW) + ty) + a % KW][VW * (16 * c + tx) + e] : 0.f;
+  auto put_state = [&]() {
+#pragma unroll
+    for (int a = 0; a < NK; ++a)
+#pragma unroll
+      for (int c = 0; c < NV; ++c) sts<VW>(&s.st[KW * (TY * (a / KW) + ty) + a % KW][VW * (16 * c + tx)], &X[a][c * VW]);
+  };
+
   for (int it = 0; it < w.nch; ++it) {
     const int c0 = back ? w.nch - 1 - it : it;
     const int t0 = w.begin + c0 * kC, n = min(kC, w.end - t0);
     const long long row = (base + t0) * D;
     if (!kEarly) fetch(it);
-    if (!SUMS) q.stash(s.q);
-    k.stash(s.k);
+    if (!SUMS) {
+      q.stash(s.q);
+      k.stash(s.k);
+      put_state();
+    }
+    k.stash(s.wk, [&](int j) { return j < n ? s.pw[back ? j + 1 : n - 1 - j] : 0.f; });
     v.stash(s.v);
     if (kEarly && it + 1 < w.nch) fetch(it + 1);
-    if (!SUMS) {
-#pragma unroll
-      for (int a = 0; a < NK; ++a)
-#pragma unroll
-        for (int c = 0; c < NV; ++c)
-#pragma unroll
-          for (int e = 0; e < VW; ++e) s.st[ty + 16 * a][16 * VW * c + VW * tx + e] = X[a][c * VW + e];
-    }
-    if (threadIdx.x == 0) {
-      const double l = decay_pow(g, n);
-      s.carry[0] = (float)l;
-      s.carry[1] = (float)(l - (double)(float)l);
-    }
     __syncthreads();
     if (!SUMS) {
-      // the scores: rows ty + 16 r, columns tx + 16 c
-      float sc[4][4] = {};
+      // the scores: rows ty + TY r, columns tx + 16 c
+      float sc[R][4] = {};
 #pragma unroll 4
-      for (int k = 0; k < D; k += 4) {
-        float a[4][4], b[4][4];
+      for (int x = 0; x < D; x += 4) {
+        float a[R][4], b[4][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) lds<4>(&s.q[ty + 16 * r][k], a[r]);
+        for (int r = 0; r < R; ++r) lds<4>(&s.q[ty + TY * r][x], a[r]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) lds<4>(&s.k[tx + 16 * r][k], b[r]);
+        for (int c = 0; c < 4; ++c) lds<4>(&s.k[tx + 16 * c][x], b[c]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
+          for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int c = 0; c < 4; ++c) sc[r][c] = fmaf(a[r][e], b[c][e], sc[r][c]);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int i = ty + 16 * r, j = tx + 16 * c, gap = back ? j - i : i - j;
+          const int i = ty + TY * r, j = tx + 16 * c, gap = back ? j - i : i - j;
           s.p[i][j] = gap >= 0 && j < n ? sc[r][c] * s.pw[gap] : 0.f;
         }
       __syncthreads();
-      // the outputs: rows 4 ty + r, value channels as the state's
-      float o[4][NV * VW] = {};
+      // the outputs: rows as the scores', value channels as the state's
+      float o[R][NV * VW] = {};
+      auto product = [&](const float *a0, int lda, const float (*b0)[D + 4], int len) {
 #pragma unroll 2
-      for (int k = 0; k < D; k += 4) {
-        float a[4][4];
+        for (int x = 0; x < len; x += 4) {
+          float a[R][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) lds<4>(&s.q[4 * ty + r][k], a[r]);
+          for (int r = 0; r < R; ++r) lds<4>(a0 + (ty + TY * r) * lda + x, a[r]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int c = 0; c < NV; ++c) {
-            float b[VW];
-            lds<VW>(&s.st[k + e][16 * VW * c + VW * tx], b);
+            for (int c = 0; c < NV; ++c) {
+              float b[VW];
+              lds<VW>(&b0[x + e][VW * (16 * c + tx)], b);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+              for (int r = 0; r < R; ++r)
 #pragma unroll
-              for (int x = 0; x < VW; ++x) o[r][c * VW + x] = fmaf(a[r][e], b[x], o[r][c * VW + x]);
-          }
-      }
+                for (int y = 0; y < VW; ++y) o[r][c * VW + y] = fmaf(a[r][e], b[y], o[r][c * VW + y]);
+            }
+        }
+      };
+      product(&s.q[0][0], D + 4, s.st, D);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 4 * ty + r;
+      for (int r = 0; r < R; ++r) {
+        const int i = ty + TY * r;
         const float f = i < n ? s.pw[back ? n - 1 - i : i + 1] : 0.f;
 #pragma unroll
         for (int x = 0; x < NV * VW; ++x) o[r][x] *= f;
       }
-#pragma unroll 2
-      for (int j = 0; j < kC; j += 4) {
-        float a[4][4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) lds<4>(&s.p[4 * ty + r][j], a[r]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int c = 0; c < NV; ++c) {
-            float b[VW];
-            lds<VW>(&s.v[j + e][16 * VW * c + VW * tx], b);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-              for (int x = 0; x < VW; ++x) o[r][c * VW + x] = fmaf(a[r][e], b[x], o[r][c * VW + x]);
-          }
-      }
+      product(&s.p[0][0], kC + 4, s.v, kC);
       TO *out = (TO *)p.t[op.o] + row;
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (4 * ty + r < n) {
+      for (int r = 0; r < R; ++r)
+        if (ty + TY * r < n) {
 #pragma unroll
           for (int c = 0; c < NV; ++c)
 #pragma unroll
             for (int x = 0; x < VW; ++x)
-              store_val(out + (long long)(4 * ty + r) * D + 16 * VW * c + VW * tx + x, o[r][c * VW + x]);
+              store_val(out + (long long)(ty + TY * r) * D + VW * (16 * c + tx) + x, o[r][c * VW + x]);
         }
     }
     // the state behind the chunk
     float u[NK][NV * VW] = {};
-#pragma unroll 2
+#pragma unroll 4
     for (int j = 0; j < kC; ++j) {
-      const float wj = j < n ? s.pw[back ? j + 1 : n - 1 - j] : 0.f;
-      float b[NV * VW];
+      float a[NK], b[NV * VW];
 #pragma unroll
-      for (int c = 0; c < NV; ++c) {
-        float y[VW];
-        lds<VW>(&s.v[j][16 * VW * c + VW * tx], y);
+      for (int c = 0; c < NKV; ++c) lds<KW>(&s.wk[j][KW * (TY * c + ty)], *reinterpret_cast<float(*)[KW]>(&a[c * KW]));
 #pragma unroll
-        for (int x = 0; x < VW; ++x) b[c * VW + x] = wj * y[x];
-      }
+      for (int c = 0; c < NV; ++c) lds<VW>(&s.v[j][VW * (16 * c + tx)], *reinterpret_cast<float(*)[VW]>(&b[c * VW]));
 #pragma unroll
-      for (int a = 0; a < NK; ++a) {
-        const float kk = s.k[j][ty + 16 * a];
+      for (int y = 0; y < NK; ++y)
 #pragma unroll
-        for (int x = 0; x < NV * VW; ++x) u[a][x] = fmaf(kk, b[x], u[a][x]);
-      }
+        for (int x = 0; x < NV * VW; ++x) u[y][x] = fmaf(a[y], b[x], u[y][x]);
     }
-    const float l0 = s.carry[0], l1 = s.carry[1];
+    const float l0 = s.carry[c0 == w.nch - 1][0], l1 = s.carry[c0 == w.nch - 1][1];
 #pragma unroll
     for (int a = 0; a < NK; ++a)
 #pragma unroll
@@ -264,12 +277,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
 
   float *dst = SUMS ? p.ws + blockIdx.x * DD : (fin && op.s_out ? op.s_out + w.bh * DD : nullptr);
   if (dst) {
-#pragma unroll
-    for (int a = 0; a < NK; ++a)
-#pragma unroll
-      for (int c = 0; c < NV; ++c)
-#pragma unroll
-        for (int e = 0; e < VW; ++e) s.st[ty + 16 * a][16 * VW * c + VW * tx + e] = X[a][c * VW + e];
+    put_state();
     __syncthreads();
     for (int e = threadIdx.x; e < D * D; e += kThreads) dst[e] = s.st[e % D][e / D];
   }
@@ -277,52 +285,35 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
 
 // ws[part] becomes the state in front of that part on the walk: it held what
 // the part itself adds.
-__global__ void __launch_bounds__(256) decay_prefix_kernel(const DecayArgs p, int dd4) {
+__global__ void __launch_bounds__(256) decay_prefix_kernel(const DecayArgs p, int dd) {
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long pair = i / dd4;
+  const long long pair = i / dd;
   launch_dependents();
   if (pair >= p.nsums * p.BH) return;
-  const int e = (int)(i % dd4) * 4;
+  const int e = (int)(i % dd);
   const DecayWork w = decay_work(p, pair * p.nseg, false);
   const DecayOp &op = p.op[w.op];
-  const long long dd = (long long)dd4 * 4;
   const float g = p.g[w.h];
   const int plen = p.seglen / p.nsub, last = decay_last_part(p, w.len);
   // parts to pass up to the final segment's first
   const int count = op.back ? last - min(p.nsub - 1, last) : w.last_seg * p.nsub;
   const double full = decay_pow(g, plen), tail = decay_pow(g, w.len - (long long)last * plen);
+  const int r = e / p.d, c = e % p.d;
+  double s = op.s_in ? op.s_in[w.bh * dd + (op.s_in_t ? c * p.d + r : e)] : 0.f;
   wait_for_launches();
-  double s[4] = {0.0, 0.0, 0.0, 0.0};
-  if (op.s_in) {
-    const float *src = op.s_in + w.bh * dd;
-    if (op.s_in_t) {
-      const int r = e / p.d, c = e % p.d;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) s[x] = src[(c + x) * p.d + r];
-    } else {
-      const float4 x = *reinterpret_cast<const float4 *>(src + e);
-      s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
-    }
-  }
-  float *ws = p.ws + pair * (p.nseg * p.nsub) * dd + e;
-  constexpr int kAhead = 8;  // parts in flight
+  const int step = op.back ? -dd : dd;
+  float *ws = p.ws + (pair * (p.nseg * p.nsub) + (op.back ? last : 0)) * dd + e;
+  constexpr int kAhead = 16;  // parts in flight
   for (int n0 = 0; n0 <= count; n0 += kAhead) {
-    float4 u[kAhead];
+    float u[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) u[x] = n0 + x < count ? ws[(long long)(n0 + x) * step] : 0.f;
 #pragma unroll
     for (int x = 0; x < kAhead; ++x) {
-      const int n = n0 + x, part = op.back ? last - n : n;
-      u[x] = n < count ? *reinterpret_cast<const float4 *>(ws + part * dd) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      const int n = n0 + x, part = op.back ? last - n : n;
+      const int n = n0 + x;
       if (n > count) break;
-      *reinterpret_cast<float4 *>(ws + part * dd) = make_float4((float)s[0], (float)s[1], (float)s[2], (float)s[3]);
-      const double l = part == last ? tail : full;
-      s[0] = fma(s[0], l, (double)u[x].x);
-      s[1] = fma(s[1], l, (double)u[x].y);
-      s[2] = fma(s[2], l, (double)u[x].z);
-      s[3] = fma(s[3], l, (double)u[x].w);
+      ws[(long long)n * step] = (float)s;
+      s = fma(s, (op.back ? last - n : n) == last ? tail : full, (double)u[x]);
     }
   }
 }
@@ -476,9 +467,9 @@ cudaError_t launch_decay_simt(const DecayArgs &a, int in_dtype, int out_dtype, b
 }
 
 cudaError_t launch_decay_prefix(const DecayArgs &a, cudaStream_t st) {
-  const int dd4 = a.d * a.d / 4;
-  const long long n = a.nsums * a.BH * dd4;
-  return launch_after(decay_prefix_kernel, (n + 255) / 256, 256, 0, st, true, a, dd4);
+  const int dd = a.d * a.d;
+  const long long n = a.nsums * a.BH * dd;
+  return launch_after(decay_prefix_kernel, (n + 255) / 256, 256, 0, st, true, a, dd);
 }
 
 cudaError_t launch_decay_step(const void *Q, const void *K, const void *V, const float *g, const int32_t *active,
