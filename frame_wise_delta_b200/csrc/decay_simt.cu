@@ -12,6 +12,15 @@
 // Powers with whole exponents >= 0 only, each at most 1, so nothing overflows.
 // All sums are in float32; everything outside j <= i or behind the last token
 // is selected away, not multiplied by 0.
+//
+// Per chunk four products of 64 x 64 x d or 64 x d x d, 4 x 4 values a thread,
+// from shared memory. What bounds it is the latency of that memory under 8 to
+// 16 warps per SM: about 2 of 4 instructions per cycle are issued and a third
+// of the FMA pipe is used; 16 warps with half the values each, packed pairs of
+// FMAs over transposed tiles (half the instructions), more CTAs per SM at d <=
+// 32 and fetching ahead at d = 128 were all no faster. Measured, float32: 4
+// heads of 5120 tokens, d = 64, 58 us (alone: state pass 15 us, join 10 us,
+// walk of two chunks per CTA 48 us); 2 x 8 heads of 2000 tokens, d = 128, 162 us.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -284,36 +293,75 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
 }
 
 // ws[part] becomes the state in front of that part on the walk: it held what
-// the part itself adds.
+// the part itself adds. A thread takes V neighbouring values of a pair's state
+// through the parts in 64 bits: a chain of dependent loads and FMAs, so kAhead
+// of the loads are in flight at once, behind a start of several us (lengths,
+// decay, powers: worked out by two threads for the block). So one value a
+// thread and the shortest chain where all blocks run at a time, four where they
+// would come in waves. Alone, one against four: 10 and 17 us for 40 parts of 4 x
+// 64 x 64 values, 34 and 13 us for 4 parts of 48 x 128 x 128.
+template <int V>
 __global__ void __launch_bounds__(256) decay_prefix_kernel(const DecayArgs p, int dd) {
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long pair = i / dd;
+  __shared__ struct {
+    const float *src;
+    float *ws;
+    double full, tail;
+    int count, last, back, tr;
+  } b;
+  const int per = (dd + 256 * V - 1) / (256 * V), pair = blockIdx.x / per, e = (blockIdx.x % per * 256 + threadIdx.x) * V;
   launch_dependents();
-  if (pair >= p.nsums * p.BH) return;
-  const int e = (int)(i % dd);
-  const DecayWork w = decay_work(p, pair * p.nseg, false);
-  const DecayOp &op = p.op[w.op];
-  const float g = p.g[w.h];
-  const int plen = p.seglen / p.nsub, last = decay_last_part(p, w.len);
-  // parts to pass up to the final segment's first
-  const int count = op.back ? last - min(p.nsub - 1, last) : w.last_seg * p.nsub;
-  const double full = decay_pow(g, plen), tail = decay_pow(g, w.len - (long long)last * plen);
-  const int r = e / p.d, c = e % p.d;
-  double s = op.s_in ? op.s_in[w.bh * dd + (op.s_in_t ? c * p.d + r : e)] : 0.f;
-  wait_for_launches();
-  const int step = op.back ? -dd : dd;
-  float *ws = p.ws + (pair * (p.nseg * p.nsub) + (op.back ? last : 0)) * dd + e;
-  constexpr int kAhead = 16;  // parts in flight
-  for (int n0 = 0; n0 <= count; n0 += kAhead) {
-    float u[kAhead];
+  if (threadIdx.x % 32 == 0 && threadIdx.x < 64) {
+    const DecayWork w = decay_work(p, (long long)pair * p.nseg, false);
+    const DecayOp &op = p.op[w.op];
+    const int plen = p.seglen / p.nsub, last = decay_last_part(p, w.len);
+    const float g = p.g[w.h];
+    if (threadIdx.x == 0) {
+      b.src = op.s_in ? op.s_in + w.bh * dd : nullptr;
+      b.ws = p.ws + ((long long)pair * (p.nseg * p.nsub) + (op.back ? last : 0)) * dd;
+      b.full = decay_pow(g, plen);
+      // parts to pass up to the final segment's first
+      b.count = op.back ? last - min(p.nsub - 1, last) : w.last_seg * p.nsub;
+      b.last = last;
+      b.back = op.back;
+      b.tr = op.s_in_t;
+    } else {
+      b.tail = decay_pow(g, w.len - (long long)last * plen);
+    }
+  }
+  __syncthreads();
+  const int count = b.count, last = b.back ? 0 : b.last;  // the step that passes the sequence's last part
+  const double full = b.full, tail = b.tail;
+  if (e >= dd) return;
+  double s[V];
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x) u[x] = n0 + x < count ? ws[(long long)(n0 + x) * step] : 0.f;
+  for (int y = 0; y < V; ++y) {
+    const int r = (e + y) / p.d, c = (e + y) % p.d;
+    s[y] = b.src ? b.src[b.tr ? c * p.d + r : e + y] : 0.f;
+  }
+  const long long step = b.back ? -dd : dd;
+  float *ws = b.ws + e;
+  wait_for_launches();
+  constexpr int kAhead = V == 1 ? 16 : 8;  // parts in flight
+  for (int n0 = 0; n0 <= count; n0 += kAhead) {
+    float u[kAhead][V];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      if (n0 + x < count)
+        lds<V>(ws + (n0 + x) * step, u[x]);
+      else
+        for (int y = 0; y < V; ++y) u[x][y] = 0.f;
+    }
 #pragma unroll
     for (int x = 0; x < kAhead; ++x) {
       const int n = n0 + x;
       if (n > count) break;
-      ws[(long long)n * step] = (float)s;
-      s = fma(s, (op.back ? last - n : n) == last ? tail : full, (double)u[x]);
+      float o[V];
+#pragma unroll
+      for (int y = 0; y < V; ++y) {
+        o[y] = (float)s[y];
+        s[y] = fma(s[y], n == last ? tail : full, (double)u[x][y]);
+      }
+      sts<V>(ws + n * step, o);
     }
   }
 }
@@ -345,6 +393,9 @@ cudaError_t launch_simt_d(const DecayArgs &a, cudaStream_t st) {
 // S, kLanes lanes to a row and 16 bytes per lane and load, so each load of a
 // warp covers full 128-byte lines; the row's product with q is summed over its
 // lanes by shuffles.
+// Measured: 72 of 96 sequences x 24 states of 128 x 128 in 55 us (49 us of it
+// the kernel), 85 % of a plain copy's rate; the 24 states of one sequence take
+// 5 us, a launch and two reads behind one another.
 constexpr int kStepThreads = 128;
 template <typename TI, typename TO, int D>
 __global__ void __launch_bounds__(kStepThreads)
@@ -420,8 +471,11 @@ DecaySplit decay_split(long long pairs, long long sums, long long n, int slots, 
   // join. Ragged sequences are half full on average, and the CTAs of short
   // ones leave their place at once: then the longest walk or half of the whole
   // work counts, whichever is more.
-  // A launch and a start cost the tensor-core kernel (1.6 us a chunk) several
+  // A launch and a start cost the tensor-core kernel (1.2 to 2 us a chunk) several
   // chunks' time, the CUDA-core one (10 us) less than one.
+  // Measured: 24 heads of 102 816 tokens, d = 128: 6 segments 0.85 ms (a single
+  // one would be 1607 chunks of 1.7 us in a row, 2.7 ms); 8 x 16 ragged heads of
+  // up to 4099 tokens, d = 64: a single segment 82 us, two 92 us.
   const long long chunks = n > 0 ? (n + kDecayC - 1) / kDecayC : 1;
   DecaySplit best{1, (int)(chunks * kDecayC), 1};
   if (pairs > 8LL * slots) return best;  // several waves of whole walks
@@ -468,8 +522,9 @@ cudaError_t launch_decay_simt(const DecayArgs &a, int in_dtype, int out_dtype, b
 
 cudaError_t launch_decay_prefix(const DecayArgs &a, cudaStream_t st) {
   const int dd = a.d * a.d;
-  const long long n = a.nsums * a.BH * dd;
-  return launch_after(decay_prefix_kernel, (n + 255) / 256, 256, 0, st, true, a, dd);
+  const long long pairs = a.nsums * a.BH, blocks = pairs * (dd / 256);
+  if (blocks <= 8 * 148) return launch_after(decay_prefix_kernel<1>, blocks, 256, 0, st, true, a, dd);
+  return launch_after(decay_prefix_kernel<4>, pairs * ((dd + 1023) / 1024), 256, 0, st, true, a, dd);
 }
 
 cudaError_t launch_decay_step(const void *Q, const void *K, const void *V, const float *g, const int32_t *active,

@@ -36,6 +36,20 @@
 //   warps 28..31: the outputs
 // Many warps with little each: every role is a chain of dependent steps on the way from one chunk
 // to the next, so it is the length of a warp's share that counts.
+//
+// What bounds it: a chunk costs the tensor pipe 1500 cycles at d = 128 (900 at d <= 64, where half of the
+// lanes are idle), and the warps together about 7000 instructions, in chains of TMEM reads, waits and
+// products that take 2000 to 2700 cycles from one chunk to the next. Measured at d = 128 in bf16:
+// 4 x 24 heads of 512 tokens 24 us (8 chunks each, 1.5 us a chunk and the start); 24 heads of 102 816
+// tokens 0.68 ms alone (pass for the segments' states 0.22 ms, join 0.01, walk 0.45; 2.5 GB in and out, 3.4
+// GB moved, 5.0 TB/s) and 0.79 to 0.89 ms one after another, when they draw 995 W and the clock falls from
+// 1965 to 1400 MHz, so that it is the energy of a chunk that counts; the gradients of 20 160 tokens 0.33 ms
+// alone, 0.40 in a row.
+// At d = 64, 8 x 16 ragged heads of up to 4099 tokens 82 us, the longest walk's 65 chunks.
+// Tried at equal or less speed: the state and the outputs in two TMEM buffers at d = 64 (84 us), two
+// output tiles in shared memory (0 to 1 % at three stages of loads), outputs by the state's warps (10 %
+// slower), the scores issued by P's warp, one warp for all products in a fixed order (2 % slower),
+// three stages of loads instead of four (1 %).
 // SUMS: only what a segment adds to the state (from zero), for the walk's later segments.
 // Every wait is bounded.
 #include <cudaTypedefs.h>

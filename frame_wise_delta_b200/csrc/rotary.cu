@@ -17,6 +17,12 @@
 // pairs when they are interleaved, the same stretch of both halves otherwise.
 // Sections that do not start on such a stretch take the widest one that divides
 // every section's half.
+//
+// Measured: Q and K of 102 816 tokens x 24 heads x 128 channels in bf16, 2.5 GB
+// moved, 0.40 ms (6.3 TB/s, 97 % of a plain copy's rate); Q, K and V of 5040
+// tokens, token-major, in stretches of 8 bytes, 42 us (186 MB, 4.5 TB/s): there
+// the angles cost about as much as turning five heads. Sixteen tokens in
+// float32 and the like are one launch, 5 us behind 12 us of the caller's.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -160,9 +166,10 @@ template <typename T, int PW, bool INTER>
 cudaError_t launch_t(const RotaryArgs &a, cudaStream_t st) {
   // tokens per block: enough for one unit per thread, 8 at least (the angles
   // of a block are shared by all heads, so few tokens per block recompute
-  // nothing); the (tensor, head) slices are spread over blocks until the card
-  // has several waves of them, as long as eight slices share a block's angles,
-  // and then until every SM has its four blocks
+  // nothing); the (tensor, head) slices are spread over blocks until each SM
+  // gets eight of them, as long as eight slices share a block's angles, and
+  // then until every SM has four. (Three tensors of 5040 tokens x 24 heads:
+  // 42 us with eight blocks per SM, 43 us with twelve, 49 us with sixteen.)
   const int P = a.d / 2, UR = P / PW;
   int tokens = (kThreads + UR - 1) / UR;
   if (tokens < 8) tokens = 8;
@@ -170,7 +177,7 @@ cudaError_t launch_t(const RotaryArgs &a, cudaStream_t st) {
   const long long tiles = (a.N + tokens - 1) / tokens;
   const int all = a.nio * a.H;
   int parts = 1;
-  while (parts * 8 < all && tiles * a.B * parts < 16 * 148) ++parts;
+  while (parts * 8 < all && tiles * a.B * parts < 8 * 148) ++parts;
   while (parts < all && tiles * a.B * parts < 4 * 148) ++parts;
   const int slices = (all + parts - 1) / parts;
   const dim3 grid((unsigned)tiles, (unsigned)((all + slices - 1) / slices), (unsigned)a.B);
