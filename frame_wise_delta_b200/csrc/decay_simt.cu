@@ -162,9 +162,16 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
   }
   // by way of shared memory, so that memory is read along its rows
   if (src) {
-    for (int e = threadIdx.x; e < D * D; e += kThreads) {
-      const int r = e / D, c = e % D;
-      s.st[tr ? r : c][tr ? c : r] = src[e];
+    constexpr int kAhead = D * D / kThreads < 16 ? D * D / kThreads : 16;  // loads in flight
+    for (int e0 = threadIdx.x; e0 < D * D; e0 += kAhead * kThreads) {
+      float y[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) y[x] = src[e0 + x * kThreads];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const int e = e0 + x * kThreads, r = e / D, c = e % D;
+        s.st[tr ? r : c][tr ? c : r] = y[x];
+      }
     }
   }
   __syncthreads();
