@@ -487,6 +487,31 @@ def test_segments_summed_in_parts():
     _state_near(_np(ds), ref_ds)
 
 
+@pytest.mark.parametrize("di,n", [("bf16", 3100), ("f32", 1100)])
+def test_many_heads_in_segments(di, n):
+    """24 heads of 128 channels, long enough for segments (their join then takes four values a thread),
+    ragged; some of the heads against the definition."""
+    B, H, d, pick = 2, 24, 128, [0, 11, 23]
+    lens = [n, n - 777]
+    x = _inputs(21, B, H, 1, n, d, di, names="qkvo")
+    s = vdn.make_shape(B, H, 1, n, d, 0, in_dtype=di)
+    assert vdn.vdn_decay_attn_workspace_bytes(s) > 0
+    o, s1 = _attn(s, x, lens)
+    out, ds = _backward(s, x, lens)
+    for b in range(B):
+        q, k, v, do = (_flat(x[c][b:b + 1, pick, :, :lens[b]]) for c in "qkvo")
+        s0, z, g = _np(x["s"][b:b + 1, pick]), _np(x["z"][b:b + 1, pick]), _np(x["g"][pick])
+        ref, ref_s = tok.decay_attn(q, k, v, g, None, s0)
+        *refs, ref_ds = tok.decay_attn_backward(q, k, v, g, do, None, s0, z)
+        tr = lambda t: np.swapaxes(t, -1, -2)  # noqa: E731
+        scales = [_scales(q, k, v, g, None, s0), _scales(do, v, k, g, None, tr(s0)),
+                  _scales(v, do, q, g, None, tr(z), back=True), _scales(k, q, do, g, None, z, back=True)]
+        for got, want, sc in zip([o, *out], [ref, *refs], scales):
+            _near(_flat(got[b:b + 1, pick, :, :lens[b]]), want, sc, di, n, d)
+        _state_near(_np(s1[b:b + 1, pick]), ref_s)
+        _state_near(_np(ds[b:b + 1, pick]), ref_ds)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_steep_decays(d):
     """Heads that forget within a chunk, on either side of each of the kernel's forms, forward and backward."""
