@@ -46,10 +46,10 @@
 // 1965 to 1400 MHz, so that it is the energy of a chunk that counts; the gradients of 20 160 tokens 0.33 ms
 // alone, 0.40 in a row.
 // At d = 64, 8 x 16 ragged heads of up to 4099 tokens 82 us, the longest walk's 65 chunks.
-// Tried at equal or less speed: the state and the outputs in two TMEM buffers at d = 64 (84 us), two
-// output tiles in shared memory (0 to 1 % at three stages of loads), outputs by the state's warps (10 %
-// slower), the scores issued by P's warp, one warp for all products in a fixed order (2 % slower),
-// three stages of loads instead of four (1 %).
+// Tried at equal or less speed: the state and the outputs in two TMEM buffers at d = 64 (85 us, with two
+// output tiles in shared memory 90), P by the warps of the other half of the lanes at d = 64 (84 us), outputs
+// by the state's warps (10 % slower), the scores issued by P's warp, one warp for all products in a fixed
+// order (2 % slower), three stages of loads instead of four (1 %).
 // SUMS: only what a segment adds to the state (from zero), for the walk's later segments.
 // Every wait is bounded.
 #include <cudaTypedefs.h>
