@@ -81,6 +81,7 @@ struct Cfg {
   static constexpr uint32_t kTabFloats = 2 * 2 * kC + 72 + 8 + 16;  // w, f per set; l^n; carries and 2^c, 2^-c; l^-n
   static constexpr uint32_t kOffBar = kOffTab + 4 * kTabFloats;
   static constexpr uint32_t kBars = 2 * kStages + 14;
+  static_assert(kBars <= 32, "a lane each");
   static constexpr size_t kSmem = 1024 + kOffBar + 8 * kBars + 16;
   // TMEM columns
   static constexpr uint32_t kX = 0, kU = DP / 2, kO = kU + DP, kSC = kO + kC, kVT = kSC + kC;
@@ -279,6 +280,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  constexpr int loads = SUMS ? 3 : 2;  // the warp that loads; it sets up the barriers, one per lane
+  if (warp == loads) {
+    constexpr int S = F::kStages;
+    const int r = lane - 2 * S;
+    // p_ready; kv_ok: the values are there, U has been read; qx_ok: the state is there, O has been read
+    const int n = r < 0              ? (lane < S || SUMS ? 1 : 2)
+                  : r >= 1 && r <= 3 ? 64
+                  : r == 4 || r == 5 ? 6 * DP
+                  : r == 10          ? 5 * DP
+                  : r == 12          ? 2
+                                     : 1;
+    if (lane < 2 * S + 13) mbar_init(full0 + 8 * lane, n);
+    if (lane == 0) *abort = 0;
+    fence_barrier_init();
+    __syncwarp();
+  }
+
   const DecayWork w = decay_work(p, blockIdx.x, SUMS);
   const DecayOp &op = p.op[w.op];
   const int back = pinned(op.back);
@@ -288,13 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nch = pinned(w.nch), d = pinned(p.d);
   const int tail = pinned(w.end - w.begin - (nch - 1) * kC);  // rows of the segment's last chunk
   const float g = p.g[w.h];
-  // 0: l^64 >= 2^-90, values and state times 2^c; 1: l^15 >= 2^-100; 2: steeper still
-  const int steep = pinned((double)g * kC >= -62.383246250395077 ? 0 : (double)g * 15 >= -69.3 ? 1 : 2);
   const uint32_t smem_a = (uint32_t)pinned((int)smem_u32(smem)), tab_a = smem_a + F::kOffTab;
   auto chunk_at = [&](int it) { return back ? nch - 1 - it : it; };
   auto rows_of = [&](int c) { return c == nch - 1 ? tail : kC; };
 
-  const int loads = (SUMS ? 3 : 2);  // the warp that loads
   const CUtensorMap *mq = &maps.m[op.q], *mk = &maps.m[op.k], *mv = &maps.m[op.v];
   auto load = [&](int it) {
     const uint32_t dst = smem_a + (it % F::kStages) * F::kStageBytes, fb = full0 + 8 * (it % F::kStages);
@@ -310,31 +325,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   };
-  // it sets up the barriers and starts on the first tiles before anything else
+  // it starts on the first tiles before anything else
   if (warp == loads) {
-    if (lane == 0) {
-      for (int s = 0; s < F::kStages; ++s) {
-        mbar_init(full0 + 8 * s, 1);
-        mbar_init(empty0 + 8 * s, SUMS ? 1 : 2);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(p_ready + 8 * i, 64);
-        mbar_init(kv_ok + 8 * i, 6 * DP);  // the values are there, U has been read
-        mbar_init(kv_full + 8 * i, 1);
-        mbar_init(pv_done + 8 * i, 1);
-      }
-      mbar_init(sc_full, 1);
-      mbar_init(sc_free, 64);
-      mbar_init(qx_ok, 5 * DP);  // the state is there, O has been read
-      mbar_init(qx_done, 1);
-      mbar_init(drain, 2);
-      *abort = 0;
-      fence_barrier_init();
-    }
-    __syncwarp();
     for (int it = 0; it < nch && it < F::kStages; ++it) load(it);
   }
   if (warp == 3) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  // 0: l^64 >= 2^-90, values and state times 2^c; 1: l^15 >= 2^-100; 2: steeper still
+  const int steep = pinned((double)g * kC >= -62.383246250395077 ? 0 : (double)g * 15 >= -69.3 ? 1 : 2);
   const int c2 = steep ? 0 : (int)((double)g * kC * -0.96179669392597561);  // 2 / (3 ln 2)
   // the weights of whole chunks (set 0) and of the segment's last one (set 1)
   if (threadIdx.x < 2 * kC) {
