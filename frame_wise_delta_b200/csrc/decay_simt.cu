@@ -19,8 +19,8 @@
 // of the FMA pipe is used; 16 warps with half the values each, packed pairs of
 // FMAs over transposed tiles (half the instructions), more CTAs per SM at d <=
 // 32 and fetching ahead at d = 128 were all no faster. Measured, float32: 4
-// heads of 5120 tokens, d = 64, 58 us (alone: state pass 15 us, join 10 us,
-// walk of two chunks per CTA 48 us); 2 x 8 heads of 2000 tokens, d = 128, 162 us.
+// heads of 5120 tokens, d = 64, 45 us; 2 x 8 heads of 2000 tokens, d = 128,
+// 144 us.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -33,8 +33,10 @@ namespace {
 constexpr int kC = kDecayC;
 
 constexpr int kThreads = 256;
-// CTAs per SM, by shared memory and registers.
-constexpr int simt_ctas(int d) { return d == 128 ? 1 : 2; }
+// CTAs per SM. At d >= 64 one, with 255 registers a thread to read ahead into
+// (4 heads of 5120 tokens, d = 64: 45 us, 56 us with two of 128 registers); at
+// d <= 32 two (3 x 4 ragged heads, d = 32, gradients: 23 us, 26 us with one).
+constexpr int simt_ctas(int d) { return d >= 64 ? 1 : 2; }
 
 template <int D>
 struct SimtSmem {
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
 
   const long long base = w.bh * (long long)p.N;
   // the next chunk is fetched under this one's arithmetic where registers hold it
-  constexpr bool kEarly = D <= 64;
+  constexpr bool kEarly = D <= 64 || SUMS;
   Rows<TI, D> q, k, v;
   auto fetch = [&](int it) {
     const int t0 = w.begin + (back ? w.nch - 1 - it : it) * kC, n = min(kC, w.end - t0);
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
       // the outputs: rows as the scores', value channels as the state's
       float o[R][NV * VW] = {};
       auto product = [&](const float *a0, int lda, const float (*b0)[D + 4], int len) {
-#pragma unroll 2
+#pragma unroll 4
         for (int x = 0; x < len; x += 4) {
           float a[R][4];
 #pragma unroll
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas(D)) decay_simt_kernel(cons
     }
     // the state behind the chunk
     float u[NK][NV * VW] = {};
-#pragma unroll 4
+#pragma unroll(D >= 64 ? 8 : 4)
     for (int j = 0; j < kC; ++j) {
       float a[NK], b[NV * VW];
 #pragma unroll
