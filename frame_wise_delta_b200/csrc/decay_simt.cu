@@ -14,11 +14,12 @@
 // is selected away, not multiplied by 0.
 //
 // Per chunk four products of 64 x 64 x d or 64 x d x d, 4 x 4 values a thread,
-// from shared memory. What bounds it is the latency of that memory under 8 to
-// 16 warps per SM: about 2 of 4 instructions per cycle are issued and a third
-// of the FMA pipe is used; 16 warps with half the values each, packed pairs of
-// FMAs over transposed tiles (half the instructions), more CTAs per SM at d <=
-// 32 and fetching ahead at d = 128 were all no faster. Measured, float32: 4
+// from shared memory. What bounds it is that memory, its rate (half of it is
+// used) and its latency under 8 to 16 warps per SM: about 2 of 4 instructions
+// per cycle are issued and 30 to 44 % of the FMA pipe is used. 16 warps with
+// half the values each, packed pairs of FMAs over transposed tiles (half the
+// instructions), more CTAs per SM at d <= 32 and fetching ahead in the walk at
+// d = 128 were all no faster. Measured, float32: 4
 // heads of 5120 tokens, d = 64, 45 us; 2 x 8 heads of 2000 tokens, d = 128,
 // 144 us.
 #include <cuda_bf16.h>
