@@ -184,13 +184,13 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
       a.turn[at++] = f;
     }
   }
+  const bool any = (long long)s->B * s->H * n > 0;
   if (!r->pos) {
-    if (r->grid_h < 1 || r->grid_w < 1 || (long long)r->grid_h * r->grid_w != s->U)
+    if (any && (r->grid_h < 1 || r->grid_w < 1 || (long long)r->grid_h * r->grid_w != s->U))
       return fail(VDN_ERR_INVALID, "grid %d x %d does not hold U = %d tokens", r->grid_h, r->grid_w, s->U);
     if (r->frame0 > (1LL << 52) || r->frame0 < -(1LL << 52)) return fail(VDN_ERR_INVALID, "frame0 beyond 2^52");
   }
   VDN_TRY(maybe(r->pos, "pos", 4));
-  const bool any = (long long)s->B * s->H * n > 0;
   const long long step = s->in_dtype == VDN_BF16 ? 8 : 4;
   const long long count[3] = {s->B, s->H, n};
   for (int k = 0; k < n_io; ++k) {

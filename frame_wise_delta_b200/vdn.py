@@ -375,7 +375,7 @@ def _rows(t, shape, dtype, dev, name):
         _bad(f"{name}'s channels are not contiguous")
     if shape[3] == 1:
         su = st
-    elif shape[2] > 1 and st != su * shape[3]:
+    elif shape[2] > 1 and st != su * shape[3] and t.numel():
         _bad(f"{name}'s frames do not follow each other")
     if t.get_device() != dev:
         _bad(f"{name} is not on the current CUDA device")

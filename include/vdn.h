@@ -432,7 +432,7 @@ vdn_status vdn_stream_segment_bridged(const vdn_shape *s, const void *Q,
 typedef struct {
   int32_t grid_h, grid_w;       /* token u of a frame is row u / grid_w, column
                                    u % grid_w; grid_h * grid_w = U (not used
-                                   with pos) */
+                                   with pos or without tokens) */
   int32_t dim_t, dim_h, dim_w;  /* channels of each axis: even, >= 0, their sum
                                    at most dk */
   int32_t interleaved, inverse; /* 0 or 1 */

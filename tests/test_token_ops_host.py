@@ -241,3 +241,19 @@ def test_binding_checks_types_and_shapes(L):
             vdn._rows(bad, shape, torch.bfloat16, -1, "X")
     # the call packs three vdn_rotary_io as words
     assert ctypes.sizeof(vdn.vdn_rotary_io) == 9 * 8 and vdn.vdn_rotary_io.rotate.offset == 64
+
+
+# ------------------------------------------------------- sizes of zero, binding
+@pytest.mark.parametrize("kw", [dict(U=0), dict(T=3, U=0), dict(T=0), dict(B=0), dict(H=0), dict(T=0, U=0)])
+@pytest.mark.parametrize("grid", [(5, 8), (0, 0), (0, 8)])
+def test_rotary_of_no_tokens(L, kw, grid):
+    """No tokens: nothing to turn, whatever the grid (one of zero tokens has no rows or no columns); with
+    tokens the grid has to hold them."""
+    import torch
+    s = _shape(**kw)
+    assert _rot(L, s, grid=grid)[0] == vdn.VDN_OK
+    assert _rot(L, _shape(), grid=(0, 8))[0] == vdn.VDN_ERR_INVALID
+    # the binding takes the tensors of such a call as they come
+    shape = (s.B, s.H, s.T, s.U, s.dk)
+    x = torch.empty(shape, dtype=torch.bfloat16)
+    assert vdn._rows(x, shape, torch.bfloat16, -1, "X")[0] == 0
