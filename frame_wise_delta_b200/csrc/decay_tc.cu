@@ -10,9 +10,11 @@
 // serve both sums, the scores need no weights of their own, and both terms of o_i share one accumulator.
 // 1/w_i is at most 1/l^64; values and state carry a factor 2^c, c two thirds of that range (60 at most), so
 // that values down to 1e-20 keep all of their bits under the smallest weight. A head that decays by more than 2^-90 over a chunk ("steep") would lose its
-// early values to float32's range: it takes o_i = f_i (X q_i + sum_j c_ij s_ij v_j) with f_i = max(l^{i+1}, 2^-60)
-// (back: l^{n-1-i}) and c_ij = l^{|i-j|} / f_i put on the scores; where f_i is cut off the state enters
-// with 2^-60 in place of something smaller, far below a rounding of o_i.
+// early values to float32's range: with l^{i+1} = 2^{e_i} f_i, 1 <= f_i < 2 (back: l^{n-1-i}), it takes
+//   o_i = f_i (X (2^{e_i} q_i) + sum_j c_ij s_ij v_j),   c_ij = l^{|i-j|} / f_i on the scores.
+// The power of two goes onto Q's row in shared memory, once the scores have read it: exact, and no
+// factor anywhere is above 1, so nothing overflows that the sums do not. Below 2^-126 a row takes
+// nothing of the state: |S| |q| 2^-126 is all that it loses.
 //
 // Four products per chunk, all with 128 TMEM lanes:
 //   SC[i][j]  = Q K^T                 A = Q, B = K (K-major tiles as TMA brings them; rows 64.. unused)
@@ -167,6 +169,8 @@ __device__ __forceinline__ int pinned(int x) {
 }
 
 __device__ __forceinline__ uint32_t as_u32(const __nv_bfloat162 &x) { return *reinterpret_cast<const uint32_t *>(&x); }
+// The largest power of two in x >= 0; 0 below the normal floats.
+__device__ __forceinline__ float pow2_in(float x) { return __uint_as_float(__float_as_uint(x) & 0x7F800000u); }
 // A bf16 pair as two floats (the low half first).
 __device__ __forceinline__ float2 unpack2(uint32_t x) {
   return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
@@ -330,8 +334,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = 0; it < nch && it < F::kStages; ++it) load(it);
   }
   if (warp == 3) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-  // 0: l^64 >= 2^-90, values and state times 2^c; 1: l^15 >= 2^-100; 2: steeper still
-  const int steep = pinned((double)g * kC >= -62.383246250395077 ? 0 : (double)g * 15 >= -69.3 ? 1 : 2);
+  // 0: l^64 >= 2^-90, values and state times 2^c; 1: l^64 >= 2^-126, the weights on the scores as products of
+  // two powers; 2: steeper, where one of the two could leave float32's range
+  const int steep = pinned((double)g * kC >= -62.383246250395077 ? 0 : (double)g * kC >= -87.3 ? 1 : 2);
   const int c2 = steep ? 0 : (int)((double)g * kC * -0.96179669392597561);  // 2 / (3 ln 2)
   // the weights of whole chunks (set 0) and of the segment's last one (set 1)
   if (threadIdx.x < 2 * kC) {
@@ -339,7 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *t = tab + set * 2 * kC;
     const double wx = decay_pow(g, back ? x + 1 : n - 1 - x);
     t[x] = x < n ? (float)scalbn(wx, c2) : 0.f;
-    t[kC + x] = x >= n ? 1.f : steep ? fmaxf((float)decay_pow(g, back ? n - 1 - x : x + 1), 0x1p-60f) : (float)(1.0 / scalbn(wx, c2));
+    float f = 1.f;
+    if (x < n && !steep) f = (float)(1.0 / scalbn(wx, c2));
+    if (x < n && steep) {
+      const float r = (float)decay_pow(g, back ? n - 1 - x : x + 1), p2 = pow2_in(r);
+      f = p2 > 0.f ? r / p2 : 1.f;
+    }
+    t[kC + x] = f;
   } else if (threadIdx.x < 2 * kC + kC + 1) {
     pw[threadIdx.x - 2 * kC] = (float)decay_pow(g, threadIdx.x - 2 * kC);
   } else if (threadIdx.x >= 224 && threadIdx.x < 240) {
@@ -460,8 +471,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           scores(it + 1);
         }
-        // O = X Q^T
+        // O = X Q^T (a steep head: Q as P's warps have left it)
         ok = warp_wait(qx_ok, (uint32_t)(it & 1), abort);
+        if (ok && steep) ok = warp_wait(p_ready + 8 * (it & 1), phase(it), abort);
         if (!ok) break;
         tc_fence_after();
         const uint64_t q = kmaj + stage_off(it);
@@ -525,6 +537,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
+        if (steep && i < n) {
+          // the row's power of two onto Q, which the scores have read; the lanes
+          // take the row's 16-byte pieces in turn, so that they meet no bank twice
+          const float p2 = pow2_in(lds_f(pw_a + 4 * (back ? n - 1 - i : i + 1)));
+          const float2 pp = make_float2(p2, p2);
+          // done since the scores read the tile: shows its bytes to these threads too
+          mbar_sleep(full0 + 8 * (it % F::kStages), (uint32_t)((it / F::kStages) & 1), abort);
+          const uint32_t q = smem_a + (it % F::kStages) * F::kStageBytes + i * 128;
+#pragma unroll 1
+          for (int x = 0; x < 8 * F::kPanels; ++x) {
+            const uint32_t a = q + (x >> 3) * kPanel + (((x ^ i) & 7) << 4);
+            uint4 y = lds_u4(a);
+            auto turn = [&](uint32_t z) {
+              const float2 t2 = __fmul2_rn(unpack2(z), pp);
+              return as_u32(__floats2bfloat162_rn(t2.x, t2.y));
+            };
+            sts_u4(a, turn(y.x), turn(y.y), turn(y.z), turn(y.w));
+          }
+        }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {  // 16 columns
           if ((b >> 1) == skip) continue;

@@ -493,7 +493,8 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
  * Precision: float32 sums and state. With bf16 inputs and output the products
  * run on the tensor cores: the decayed values enter the state as three bf16
  * parts (2^-24 relative); the scores, and the copy of the state that the
- * outputs of a chunk read, are rounded to bf16.
+ * outputs of a chunk read, are rounded to bf16. A decay below 2^-126 (of the
+ * state up to a token, or of one token up to another of its chunk) counts as 0.
  */
 size_t vdn_decay_attn_workspace_bytes(const vdn_shape *s);
 vdn_status vdn_decay_attn(const vdn_shape *s, const void *Q, const void *K, const void *V,

@@ -63,6 +63,22 @@ def decay_scale(q, k, v, log_decay, s_in=None, back=False, z=None):
     return m, a
 
 
+def decayed_scale(q, k, v, log_decay, lens=None, s_in=None, back=False):
+    """decay_scale with the carried state's share decayed as it is in the output:
+    A_i takes l^(i+1) |S| |q_i|, on the walk back l^(len-1-i) |S| |q_i|."""
+    m, a = decay_scale(q, k, v, log_decay, None, back)
+    if s_in is not None:
+        q = np.asarray(q, np.float64)
+        B, n = q.shape[0], q.shape[2]
+        i = np.arange(n)[None, :]
+        e = np.array(_lens(lens, B, n))[:, None] - 1 - i if back else np.broadcast_to(i + 1, (B, n))
+        g = np.asarray(log_decay, np.float64)[None, :, None]
+        with np.errstate(invalid="ignore"):
+            w = np.where(e[:, None] > 0, np.exp(g * np.maximum(e[:, None], 1)), e[:, None] == 0)
+        a = a + w[..., None] * (np.abs(q) @ np.swapaxes(np.abs(np.asarray(s_in, np.float64)), -1, -2))
+    return m, a
+
+
 def state_reads(q, k, v, log_decay, lens=None, s_in=None, back=False, chunk=64):
     """R_i = sum_k |X_vk| |q_ik|, X the state in front of token i's chunk (on the
     walk back: behind it) with its decay up to token i: what a relative error of

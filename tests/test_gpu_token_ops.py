@@ -621,3 +621,65 @@ def test_binding_refuses_other_shapes():
         args[at] = bad
         with pytest.raises(vdn.VdnError):
             vdn.vdn_decay_attn(*args)
+
+
+def _decayed(q, k, v, g, lens=None, s_in=None, back=False):
+    return *tok.decayed_scale(q, k, v, g, lens, s_in, back), tok.state_reads(q, k, v, g, lens, s_in, back)
+
+
+def _near_decayed(got, ref, scales, dt, n, d, floor):
+    """_near with the state's share of the bound decayed as in the output, and `floor` for what lies below
+    float32's range: a factor that is under 2^-126 counts as 0."""
+    m, a, r = scales
+    rows = np.isfinite(ref)
+    if dt == "bf16":
+        tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -8 * 1.01 * (m + r) + 2.0 ** -13 * a
+    else:
+        tol = 2.0 ** -24 * (d + 128 + n / 64) * a + 2.0 ** -24 * np.abs(ref)
+    off = (np.abs(got - ref) - tol - floor)[rows]
+    assert np.isfinite(got[rows]).all()
+    assert off.size == 0 or off.max() <= 0, float(off.max())
+
+
+@pytest.mark.parametrize("power", [0, 90])
+@pytest.mark.parametrize("d,dt", [(64, "bf16"), (128, "bf16"), (64, "f32")])
+def test_steep_heads_let_nothing_through(d, dt, power):
+    """Heads that forget within a chunk: what is left of the start state, however large, and of a sequence's
+    first tokens decays on as the formula says, down to float32's smallest numbers."""
+    g = [-0.98, -1.2, -1.37, -1.4, -2.5, -5.0, -12.0, float("-inf")]
+    n, f = 200, 2.0 ** power
+    x = _inputs(23, 1, len(g), 1, n, d, dt, names="qkvo", g=g)
+    x["v"][:, :, :, 3:] = 0                       # the first tokens alone write (back: the last ones)
+    x["o"][:, :, :, :n - 3] = 0
+    x["s"] *= f
+    x["z"] *= f
+    s = vdn.make_shape(1, len(g), 1, n, d, 0, in_dtype=dt)
+    o, _ = _attn(s, x)
+    out, _ = _backward(s, x)
+    q, k, v, do = (_flat(x[c]) for c in "qkvo")
+    s0, z, g = _np(x["s"]), _np(x["z"]), np.array(g, np.float32).astype(np.float64)
+    ref, _ = tok.decay_attn(q, k, v, g, None, s0)
+    *refs, _ = tok.decay_attn_backward(q, k, v, g, do, None, s0, z)
+    tr = lambda t: np.swapaxes(t, -1, -2)  # noqa: E731
+    args = [(q, k, v, s0, False), (do, v, k, tr(s0), False), (v, do, q, tr(z), True), (k, q, do, z, True)]
+    for got, want, (a, b, c, st, back) in zip([o, *out], [ref, *refs], args):
+        # a sum's d + 64 terms lose less than 2^-126 times their other factors each
+        floor = 2.0 ** -118 * tok.decay_scale(a, b, c, g, st, back)[1]
+        _near_decayed(_flat(got), want, _decayed(a, b, c, g, None, st, back), dt, n, d, floor)
+    # the head that keeps nothing knows the token itself alone, whose other factor is 0 here
+    dq, dk, dv = (_flat(t)[0, -1] for t in out)
+    assert (_flat(o)[0, -1, 3:] == 0).all() and (dq == 0).all() and (dk == 0).all() and (dv[:n - 3] == 0).all()
+
+
+def test_steep_heads_take_large_values():
+    """Values of 2^100 in heads that forget within a chunk: the same bits times 2^100."""
+    g = [-1.0, -1.38, -1.4, -6.0, float("-inf")]
+    x = _inputs(24, 1, len(g), 1, 150, 128, "bf16", names="qkvo", g=g)
+    s = vdn.make_shape(1, len(g), 1, 150, 128, 0)
+    f = 2.0 ** 100
+    y = {**x, **{c: x[c] * f for c in "vsoz"}}
+    (o, s1), (o2, s2) = _attn(s, x), _attn(s, y)
+    assert torch.equal(o * f, o2) and torch.equal(s1 * f, s2)
+    # dV and dS_in are linear in dO and dS_out, dQ and dK are products with V and S_in as well
+    (g1, d1), (g2, d2) = _backward(s, x), _backward(s, {**y, "v": x["v"], "s": x["s"]})
+    assert all(torch.equal(a * f, b) for a, b in zip([*g1, d1], [*g2, d2]))

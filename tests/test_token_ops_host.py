@@ -57,6 +57,22 @@ def test_state_reads_are_the_state_in_front():
     assert (r[1, :, 4:] == 0).all()
 
 
+def test_the_state_decays_in_the_scale():
+    """Values of one sign: the scale is the output itself, walking forward and back, forgetting heads too."""
+    q, k, v, do, g, s, z = (np.abs(x) for x in _draw(6))
+    g = np.array([0.0, -3.0, -np.inf])
+    lens = [9, 4]
+    rows = np.arange(9)[None, None, :, None] < np.array(lens)[:, None, None, None]
+    o, _ = tok.decay_attn(q, k, v, g, lens, s)
+    _, a = tok.decayed_scale(q, k, v, g, lens, s)
+    np.testing.assert_allclose(np.where(rows, a, 0), np.where(rows, o, 0), rtol=1e-12)
+    _, _, dv, _ = tok.decay_attn_backward(q, k, v, g, do, lens, s, z)
+    # dV walks back over (K, Q, dO): what lies behind a sequence's end is not part of it
+    cut = lambda x: np.where(rows, x, 0)  # noqa: E731
+    _, a = tok.decayed_scale(cut(k), cut(q), cut(do), g, lens, z, back=True)
+    np.testing.assert_allclose(cut(a), cut(dv), rtol=1e-12)
+
+
 @pytest.mark.parametrize("lens", [None, [9, 4], [0, 1]])
 def test_gradients_are_the_differences(lens):
     q, k, v, do, g, s, z = _draw(2)
