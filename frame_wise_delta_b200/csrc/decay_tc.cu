@@ -266,6 +266,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// A steep head: each valid row of Q (up to `last`) takes the power of two in its decay; 16-byte pieces,
+// two a thread. pw: l^n. A call of its own: within the state's loop its registers and instructions cost
+// the other heads 3 to 5 % (24 heads of 102 816 tokens, d = 128), by P's warps even the steep ones more
+// (8 x 16 heads of 4099 tokens, d = 64: 147 us against 136).
+__device__ __noinline__ void scale_q(uint32_t tile, uint32_t pw, int piece, int threads, int last, int back) {
+#pragma unroll
+  for (int x = 0; x < 2; ++x, piece += threads) {
+    const int row = (piece >> 3) & (kC - 1);
+    if (row <= last) {
+      const uint32_t a = tile + 16 * piece;
+      const __nv_bfloat162 p2 = __float2bfloat162_rn(pow2_in(lds_f(pw + 4 * (back ? last - row : row + 1))));
+      auto times = [&](uint32_t y) { return as_u32(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), p2)); };
+      const uint4 y = lds_u4(a);
+      sts_u4(a, times(y.x), times(y.y), times(y.z), times(y.w));
+    }
+  }
+  fence_proxy_async_smem();
+}
+
 template <int DP, bool SUMS>
 __global__ void __launch_bounds__(kThreads, 1)
     decay_tc_kernel(const __grid_constant__ DecayMaps maps, const __grid_constant__ DecayArgs p) {
@@ -471,9 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           scores(it + 1);
         }
-        // O = X Q^T (a steep head: Q as P's warps have left it)
+        // O = X Q^T (a steep head: Q as the state's warps have left it)
         ok = warp_wait(qx_ok, (uint32_t)(it & 1), abort);
-        if (ok && steep) ok = warp_wait(p_ready + 8 * (it & 1), phase(it), abort);
         if (!ok) break;
         tc_fence_after();
         const uint64_t q = kmaj + stage_off(it);
@@ -537,25 +555,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        if (steep && i < n) {
-          // the row's power of two onto Q, which the scores have read; the lanes
-          // take the row's 16-byte pieces in turn, so that they meet no bank twice
-          const float p2 = pow2_in(lds_f(pw_a + 4 * (back ? n - 1 - i : i + 1)));
-          const float2 pp = make_float2(p2, p2);
-          // done since the scores read the tile: shows its bytes to these threads too
-          mbar_sleep(full0 + 8 * (it % F::kStages), (uint32_t)((it / F::kStages) & 1), abort);
-          const uint32_t q = smem_a + (it % F::kStages) * F::kStageBytes + i * 128;
-#pragma unroll 1
-          for (int x = 0; x < 8 * F::kPanels; ++x) {
-            const uint32_t a = q + (x >> 3) * kPanel + (((x ^ i) & 7) << 4);
-            uint4 y = lds_u4(a);
-            auto turn = [&](uint32_t z) {
-              const float2 t2 = __fmul2_rn(unpack2(z), pp);
-              return as_u32(__floats2bfloat162_rn(t2.x, t2.y));
-            };
-            sts_u4(a, turn(y.x), turn(y.y), turn(y.z), turn(y.w));
-          }
-        }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {  // 16 columns
           if ((b >> 1) == skip) continue;
@@ -635,13 +634,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(qx_ok);
       };
       for (int i = 0; i < kBufU; ++i) mbar_arrive(kv_ok + 8 * i);  // nothing in U yet
-      if (!SUMS && nch > 0) publish(0);
       bool ok = true;
       uint32_t turn = 0x80000000u;
       for (int it = 0; it < nch; ++it) {
+        if (!SUMS) {
+          if (it > 0) {
+            ok = warp_wait(qx_done, (uint32_t)((it - 1) & 1), abort);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          publish(it);
+          if (steep) {
+            // P is there, so the scores have read Q (the tile's own wait shows its bytes to these threads)
+            const int s = it % F::kStages;
+            ok = warp_wait(p_ready + 8 * buf(it), phase(it), abort) &&
+                 warp_wait(full0 + 8 * s, (uint32_t)((it / F::kStages) & 1), abort);
+            if (!ok) break;
+            scale_q(smem_a + s * F::kStageBytes, tab_a + 4 * (2 * 2 * kC), part * DP + r, 4 * DP, rows_of(chunk_at(it)) - 1, back);
+          }
+          mbar_arrive(qx_ok);
+        }
         const float4 ca = lds_f4(tab_a + 4 * (2 * 2 * kC + 72 + 4 * set_of(chunk_at(it))));
         const uint32_t before = turn;
         turn += __float_as_uint(ca.z);
@@ -662,12 +676,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(kv_ok + 8 * buf(it + kBufU));
-        if (!SUMS && it + 1 < nch) {
-          ok = warp_wait(qx_done, (uint32_t)(it & 1), abort);
-          if (!ok) break;
-          tc_fence_after();
-          publish(it + 1);
-        }
       }
       if (!ok) fail(abort, p.info);
       // where it goes is found anew: kept over the loop, it would cost registers
