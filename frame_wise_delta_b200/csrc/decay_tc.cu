@@ -8,8 +8,9 @@
 //   o_i = 1/w_i (l^n X q_i + sum_j s_ij w_j v_j),   j <= i (back: j >= i),
 // since l^{i-j} = w_j / w_i and l^{i+1} = l^n / w_i (back: l^{j-i}, l^{n-1-i}). So the weighted values
 // serve both sums, the scores need no weights of their own, and both terms of o_i share one accumulator.
-// 1/w_i is at most 1/l^64; values and state carry a factor 2^c, c two thirds of that range (60 at most), so
-// that values down to 1e-20 keep all of their bits under the smallest weight. A head that decays by more than 2^-90 over a chunk ("steep") would lose its
+// 1/w_i is at most 1/l^64; values and state carry a factor 2^c, c half of that range (45 at most): sums up to
+// 2^(127-c) fit (2^82 = 5e24 in the worst head), and values down to 2^-57 = 7e-18 keep all of their bits under
+// the smallest weight. A head that decays by more than 2^-90 over a chunk ("steep") would lose its
 // early values to float32's range: with l^{i+1} = 2^{e_i} f_i, 1 <= f_i < 2 (back: l^{n-1-i}), it takes
 //   o_i = f_i (X (2^{e_i} q_i) + sum_j c_ij s_ij v_j),   c_ij = l^{|i-j|} / f_i on the scores.
 // The power of two goes onto Q's row in shared memory, once the scores have read it: exact, and no
@@ -356,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // 0: l^64 >= 2^-90, values and state times 2^c; 1: l^64 >= 2^-126, the weights on the scores as products of
   // two powers; 2: steeper, where one of the two could leave float32's range
   const int steep = pinned((double)g * kC >= -62.383246250395077 ? 0 : (double)g * kC >= -87.3 ? 1 : 2);
-  const int c2 = steep ? 0 : (int)((double)g * kC * -0.96179669392597561);  // 2 / (3 ln 2)
+  // a sequence without tokens only hands its state on, as it is
+  const int c2 = steep || nch == 0 ? 0 : (int)((double)g * kC * -0.72134752044448170);  // 1 / (2 ln 2)
   // the weights of whole chunks (set 0) and of the segment's last one (set 1)
   if (threadIdx.x < 2 * kC) {
     const int set = threadIdx.x / kC, x = threadIdx.x % kC, n = set ? tail : kC;

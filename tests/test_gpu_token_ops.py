@@ -683,3 +683,35 @@ def test_steep_heads_take_large_values():
     # dV and dS_in are linear in dO and dS_out, dQ and dK are products with V and S_in as well
     (g1, d1), (g2, d2) = _backward(s, x), _backward(s, {**y, "v": x["v"], "s": x["s"]})
     assert all(torch.equal(a * f, b) for a, b in zip([*g1, d1], [*g2, d2]))
+
+
+@pytest.mark.parametrize("n", [100, 2500])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_powers_of_two_pass_through(n, d):
+    """Values and state beyond 2^70 in heads that carry a factor inside: the same bits times that power (sums
+    here stay below 2^7 times it, under the 2^82 of the steepest of these heads)."""
+    g = [-0.01, -0.3, -0.5, -0.7, -0.97]
+    x = _inputs(25, 1, len(g), 1, n, d, "bf16", names="qkvo", g=g)
+    s = vdn.make_shape(1, len(g), 1, n, d, 0)
+    f = 2.0 ** 74
+    (o, s1), (o2, s2) = _attn(s, x), _attn(s, {**x, "v": x["v"] * f, "s": x["s"] * f})
+    assert torch.equal(o * f, o2) and torch.equal(s1 * f, s2)
+    (g1, d1), (g2, d2) = _backward(s, x), _backward(s, {**x, "o": x["o"] * f, "z": x["z"] * f})
+    assert all(torch.equal(a * f, b) for a, b in zip([*g1, d1], [*g2, d2]))
+
+
+@pytest.mark.parametrize("n", [100, 2500])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_empty_sequences_hand_their_state_on(n, dt):
+    """Any float32 state, in every kind of head, forward and back, beside a sequence with tokens."""
+    g = [0.0, -0.01, -0.5, -0.7, -0.97, -1.2, -6.0, float("-inf")]
+    x = _inputs(26, 2, len(g), 1, n, 64, dt, names="qkvo", g=g)
+    lens = [0, 70]
+    for c in "sz":
+        x[c][0] = torch.tensor([3.4e38, -1e30, 1e-30, 1e-42, 0.0, -2.5], device="cuda").repeat(len(g) * 64 * 64 // 6 + 1)[
+            :len(g) * 64 * 64].view(len(g), 64, 64)
+    s = vdn.make_shape(2, len(g), 1, n, 64, 0, in_dtype=dt)
+    o, s1 = _attn(s, x, lens)
+    out, ds = _backward(s, x, lens)
+    assert torch.equal(s1[0], x["s"][0]) and torch.equal(ds[0], x["z"][0])
+    assert all((t[0] == MARK).all() for t in (o, *out))
