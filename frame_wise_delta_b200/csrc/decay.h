@@ -152,7 +152,9 @@ struct RotaryArgs {
   long long N, frame0;
   int npairs[3];              // rotated pairs of each axis
   const int32_t *pos;         // [B, N, 3] or null
-  double turn[kRotaryPairs];  // turns per position of each pair
+  // turns per position of each pair, as a sum of two doubles
+  double turn[kRotaryPairs], turn_lo[kRotaryPairs];
+  int far;                    // positions may take 2^20 turns or more (rotary.cu)
 };
 cudaError_t launch_rotary(const RotaryArgs &a, int dtype, cudaStream_t st);
 

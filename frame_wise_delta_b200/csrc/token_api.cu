@@ -125,6 +125,31 @@ vdn_status run_decay(const vdn_shape *s, DecayArgs &a, cudaStream_t st) {
   return VDN_OK;
 }
 
+// A number of about 106 bits as a sum of two doubles (Dekker, "A floating-point
+// technique for extending the available precision", 1971), for the rotary
+// frequencies: a position of 2^52 turns them into angles with float32's accuracy.
+struct Twofold {
+  double hi, lo;
+};
+Twofold operator*(const Twofold &a, const Twofold &b) {
+  const double p = a.hi * b.hi, e = fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi), s = p + e;
+  return {s, e - (s - p)};
+}
+constexpr Twofold kInv2Pi = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
+// theta^(-1/n): the double next to it, and a Newton step on y^n theta = 1.
+Twofold inverse_root(double theta, int n) {
+  if (n <= 1) return {n ? 1.0 / theta : 1.0, 0.0};  // not used by an axis of one pair
+  const double y = pow(theta, -1.0 / n);
+  Twofold power = {1.0, 0.0}, square = {y, 0.0};
+  for (int e = n; e; e >>= 1) {
+    if (e & 1) power = power * square;
+    square = square * square;
+  }
+  const Twofold r = power * Twofold{theta, 0.0};
+  const double step = -y * ((r.hi - 1.0) + r.lo) / n;
+  return isfinite(step) ? Twofold{y, step} : Twofold{y, 0.0};
+}
+
 // y's rows may not overlap: walking its axes from the smallest stride up, each
 // stride passes the extent of those below.
 bool disjoint_rows(const long long *stride, const long long *count, int d) {
@@ -162,6 +187,7 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
   RotaryArgs a{};
   int at = 0;
   long long sum = 0;
+  double most = 0.0;  // turns per position
   for (int x = 0; x < 3; ++x) {
     if (dims[x] < 0 || dims[x] % 2) return fail(VDN_ERR_INVALID, "axis of %d channels: even and >= 0 is needed", dims[x]);
     sum += dims[x];
@@ -170,18 +196,19 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
   if (!(r->theta > 0.0) || !isfinite(r->theta)) return fail(VDN_ERR_INVALID, "theta must be positive and finite");
   if ((r->interleaved != 0 && r->interleaved != 1) || (r->inverse != 0 && r->inverse != 1))
     return fail(VDN_ERR_INVALID, "interleaved and inverse must be 0 or 1");
-  constexpr double kPi = 3.14159265358979323846;
   for (int x = 0; x < 3; ++x) {
     if (!isfinite(scales[x])) return fail(VDN_ERR_INVALID, "scale must be finite");
     a.npairs[x] = dims[x] / 2;
-    // theta^(-2 i / n): every fourth by pow, the others by a product from there
-    double near[4] = {1.0, 0.0, 0.0, 0.0}, base = 1.0;
-    for (int i = 0; i < a.npairs[x]; ++i) {
-      if (i < 4) near[i] = pow(r->theta, -2.0 * i / dims[x]);
-      if (i % 4 == 0) base = i ? pow(r->theta, -2.0 * i / dims[x]) : 1.0;
-      const double f = base * near[i % 4] * scales[x] / (2.0 * kPi);
-      if (!isfinite(f) || fabs(f) > 1e6) return fail(VDN_ERR_INVALID, "theta and scale turn a pair by more than 1e6 turns");
-      a.turn[at++] = f;
+    // theta^(-2 i / n) as powers of theta^(-2 / n)
+    const Twofold step = inverse_root(r->theta, a.npairs[x]);
+    Twofold f = {1.0, 0.0};
+    for (int i = 0; i < a.npairs[x]; ++i, f = f * step) {
+      const Twofold turn = f * Twofold{scales[x], 0.0} * kInv2Pi;
+      if (!isfinite(turn.hi) || fabs(turn.hi) > 1e6)
+        return fail(VDN_ERR_INVALID, "theta and scale turn a pair by more than 1e6 turns");
+      a.turn[at] = turn.hi;
+      most = fmax(most, fabs(turn.hi));
+      a.turn_lo[at++] = isfinite(turn.lo) ? turn.lo : 0.0;
     }
   }
   const bool any = (long long)s->B * s->H * n > 0;
@@ -232,6 +259,8 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
   a.N = n;
   a.frame0 = r->frame0;
   a.pos = r->pos;
+  const double first = fabs((double)r->frame0), last = fabs((double)r->frame0 + s->T), side = fmax(a.gw, s->U);
+  a.far = most * (r->pos ? 0x1p31 : fmax(side, fmax(first, last))) >= 0x1p20;
   VDN_CUDA(launch_rotary(a, s->in_dtype, (cudaStream_t)stream), "rotary");
   return VDN_OK;
 }

@@ -426,8 +426,10 @@ vdn_status vdn_stream_segment_bridged(const vdn_shape *s, const void *Q,
  *   y_a = x_a cos - x_b sin,  y_b = x_a sin + x_b cos,
  * (a, b) = channels (2 i, 2 i + 1) of the axis' section (interleaved = 1) or
  * (i, i + n / 2) (interleaved = 0). inverse = 1 turns the other way: the
- * transposed rotation, which is the gradient's. Angles are reduced in float64
- * and the products taken in float32, so far positions keep their accuracy.
+ * transposed rotation, which is the gradient's. Angles are formed and reduced
+ * with about 100 bits and the products taken in float32, so every position
+ * within the limits below keeps float32's accuracy (theta and the scales count
+ * as the float64 numbers that they are).
  */
 typedef struct {
   int32_t grid_h, grid_w;       /* token u of a frame is row u / grid_w, column

@@ -3,6 +3,8 @@ decay attention, its gradients), one token at a time. Arrays are [B, H, n, d];
 states [B, H, d_v, d_k]; `lens` holds the tokens of each sequence or is None."""
 from __future__ import annotations
 
+from decimal import Decimal, localcontext
+
 import numpy as np
 
 
@@ -103,6 +105,20 @@ def state_reads(q, k, v, log_decay, lens=None, s_in=None, back=False, chunk=64):
             for j in range(a, e):
                 x = x + power(j - a + 1 if back else e - 1 - j) * v[b, :, j, :, None] * k[b, :, j, None, :]
     return r
+
+
+def far_angles(pos, dim, theta, scale):
+    """pos * scale * theta^(-2 i / dim) less whole turns, [n, dim / 2], from 60 digits: whole numbers of any size."""
+    with localcontext() as c:
+        c.prec = 60
+        turn = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803483")
+        out = np.empty((len(pos), dim // 2))
+        for i in range(dim // 2):
+            step = Decimal(scale) * Decimal(theta) ** (Decimal(-2 * i) / dim)
+            for j, x in enumerate(pos):
+                a = Decimal(int(x)) * step
+                out[j, i] = a - (a / turn).to_integral_value() * turn
+    return out
 
 
 def rotary(x, pos, dims, theta, scale=(1.0, 1.0, 1.0), interleaved=True, inverse=False):

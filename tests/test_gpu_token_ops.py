@@ -715,3 +715,48 @@ def test_empty_sequences_hand_their_state_on(n, dt):
     out, ds = _backward(s, x, lens)
     assert torch.equal(s1[0], x["s"][0]) and torch.equal(ds[0], x["z"][0])
     assert all((t[0] == MARK).all() for t in (o, *out))
+
+
+FAR = [
+    # frame0, theta, scale
+    (1 << 31, 10000.0, 1.0), ((1 << 40) + 12345, 256.0, 0.5), (1234567890123, 500000.0, 1.25), ((1 << 52) - 2, 10000.0, 1.0),
+    (-(1 << 52), 10000.0, 0.1), (-(1 << 45) + 1, 1000.0, 100.0), (1 << 50, 1.0, 1.0), (1 << 52, 1e300, 1.0), (1 << 44, 0.5, 3.0),
+]
+
+
+@pytest.mark.parametrize("frame0,theta,scale", FAR)
+@pytest.mark.parametrize("inter", [True, False])
+def test_rotary_far_frames(frame0, theta, scale, inter):
+    """Every frame that a call takes, against angles from 60 digits, with the bound of the near ones: the
+    remainder of a turn, its sine and cosine and the two products in float32."""
+    T, d, dim = 3, 64, 60
+    r = np.random.default_rng(70)
+    x = torch.from_numpy(r.standard_normal((1, 2, T, 1, d))).float().cuda()
+    y = torch.empty_like(x)
+    s = vdn.make_shape(1, 2, T, 1, d, 0, in_dtype="f32")
+    vdn.vdn_rotary(s, vdn.rotary(dim, 2, 2, grid=(1, 1), interleaved=inter, frame0=frame0, theta=theta, scale=(scale, 1.0, 1.0)),
+                   [x], [y])
+    _far_near(x, y, tok.far_angles([frame0 + t for t in range(T)], dim, theta, scale), dim, inter)
+
+
+def _far_near(x, y, ang, dim, inter):
+    f, got = _flat(x)[..., :dim], _flat(y)[..., :dim]
+    a, b = (f[..., 0::2], f[..., 1::2]) if inter else (f[..., :dim // 2], f[..., dim // 2:])
+    c, s = np.cos(ang), np.sin(ang)
+    u, v = a * c - b * s, a * s + b * c
+    ref = np.stack([u, v], -1).reshape(f.shape) if inter else np.concatenate([u, v], -1)
+    assert (np.abs(got - ref) <= 2.0 ** -24 * np.abs(ref) + 2.0 ** -20 * np.abs(f).max()).all()
+
+
+@pytest.mark.parametrize("theta,scale", [(10000.0, 1.0), (256.0, 1000.0)])
+def test_rotary_far_positions(theta, scale):
+    """Given positions over the whole of int32."""
+    d, pos = 32, [2 ** 31 - 1, -(2 ** 31), 123456789, -1, 2 ** 30 + 1]
+    n = len(pos)
+    r = np.random.default_rng(71)
+    x = torch.from_numpy(r.standard_normal((1, 2, n, 1, d))).float().cuda()
+    y = torch.empty_like(x)
+    pt = torch.tensor([[[0, 0, p] for p in pos]], dtype=torch.int32, device="cuda")
+    s = vdn.make_shape(1, 2, n, 1, d, 0, in_dtype="f32")
+    vdn.vdn_rotary(s, vdn.rotary(0, 0, d, theta=theta, scale=(1.0, 1.0, scale), pos=pt), [x], [y])
+    _far_near(x, y, tok.far_angles(pos, d, theta, scale), d, True)

@@ -116,6 +116,19 @@ def test_rotary_turns_pairs():
     np.testing.assert_allclose(y[0, 0, 0, 3], x[0, 0, 0, 2] * s + x[0, 0, 0, 3] * c)
 
 
+def test_far_angles():
+    """Near positions as in float64; far ones by the sum of two nearer angles; whole turns by hand."""
+    pos = np.array([0, 1, -7, 12345])
+    a = tok.far_angles(pos, 12, 500.0, 0.75)
+    want = pos[:, None] * 0.75 * 500.0 ** (-2.0 * np.arange(6) / 12)
+    np.testing.assert_allclose(np.exp(1j * a), np.exp(1j * want), atol=1e-11)
+    assert np.abs(a).max() <= np.pi
+    far = tok.far_angles([2 ** 51 + 12345, 2 ** 51], 12, 500.0, 0.75)
+    np.testing.assert_allclose(np.exp(1j * (far[0] - far[1])), np.exp(1j * a[3]), atol=1e-11)
+    # the C library reduces by pi in full as well
+    assert abs(np.sin(tok.far_angles([2 ** 52], 2, 1.0, 1.0)[0, 0]) - np.sin(2.0 ** 52)) < 1e-15
+
+
 # ----------------------------------------------------------------- refusals
 def _p(s):
     return ctypes.cast(ctypes.pointer(s), ctypes.c_void_p)
