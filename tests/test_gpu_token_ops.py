@@ -760,3 +760,36 @@ def test_rotary_far_positions(theta, scale):
     s = vdn.make_shape(1, 2, n, 1, d, 0, in_dtype="f32")
     vdn.vdn_rotary(s, vdn.rotary(0, 0, d, theta=theta, scale=(1.0, 1.0, scale), pos=pt), [x], [y])
     _far_near(x, y, tok.far_angles(pos, d, theta, scale), d, True)
+
+
+@pytest.mark.parametrize("lens", [None, [300, 129]], ids=["whole", "ragged"])
+@pytest.mark.parametrize("d,di,do", [(128, "bf16", "bf16"), (64, "bf16", "bf16"), (16, "bf16", "bf16"), (32, "f32", "f32"),
+                                     (128, "f32", "f32"), (64, "bf16", "f32"), (32, "f32", "bf16")])
+def test_decays_within_the_decayed_bound(d, di, do, lens):
+    """Every kind of head against the bound whose state share decays with the tokens, small writes beside a
+    start state of ordinary size, so that the state's share is what an output near it consists of."""
+    g = [0.0, -1e-7, -1e-3, -0.05, -0.3, -0.65, -0.9, -1.1, -1.5, -5.0, -80.0, float("-inf")]
+    B, n = 1 if lens is None else 2, 300
+    x = _inputs(27 + d, B, len(g), 1, n, d, di, names="qkvo", g=g)
+    x["v"] *= 2.0 ** -10
+    x["o"] *= 2.0 ** -10
+    s = vdn.make_shape(B, len(g), 1, n, d, 0, in_dtype=di, out_dtype=do)
+    o, s1 = _attn(s, x, lens)
+    q, k, v, do_ = (_flat(x[c]) for c in "qkvo")
+    s0, z, g = _np(x["s"]), _np(x["z"]), np.array(g, np.float32).astype(np.float64)
+    ref, ref_s = tok.decay_attn(q, k, v, g, lens, s0)
+    keep = np.isfinite(ref)
+    q, k, v, do_ = (np.where(keep, y, 0.0) for y in (q, k, v, do_))
+    tr = lambda t: np.swapaxes(t, -1, -2)  # noqa: E731
+    cases = [(o, ref, (q, k, v, s0, False))]
+    if di == do:
+        out, ds = _backward(s, x, lens)
+        *refs, ref_ds = tok.decay_attn_backward(q, k, v, g, do_, lens, s0, z)
+        cases += list(zip(out, refs, [(do_, v, k, tr(s0), False), (v, do_, q, tr(z), True), (k, q, do_, z, True)]))
+        for h in range(len(g)):
+            assert np.linalg.norm(_np(ds)[:, h] - ref_ds[:, h]) <= 2e-6 * np.linalg.norm(ref_ds[:, h]) + 1e-36
+    for h in range(len(g)):
+        _state_near(_np(s1)[:, h], ref_s[:, h])
+    for got, want, (a, b, c, st, back) in cases:
+        floor = 2.0 ** -118 * tok.decay_scale(a, b, c, g, st, back)[1]
+        _near_decayed(_flat(got), want, _decayed(a, b, c, g, lens, st, back), do, n, d, floor)

@@ -73,6 +73,24 @@ def test_the_state_decays_in_the_scale():
     np.testing.assert_allclose(cut(a), cut(dv), rtol=1e-12)
 
 
+def test_the_decayed_scale_sees_a_leak_of_the_state():
+    """A head that forgets in a few tokens, with small writes: a share of 2^-13 of the start state in every
+    output stays within the undecayed scale's slack and breaks the decayed one's, forward and back."""
+    r = np.random.default_rng(7)
+    q, k, v = (r.standard_normal((1, 1, 60, 16)) for _ in range(3))
+    v *= 2.0 ** -13
+    g, s = np.array([-5.0]), r.standard_normal((1, 1, 16, 16))
+    for back in (False, True):
+        leak = 2.0 ** -13 * np.abs(np.einsum("bhvk,bhik->bhiv", s, q))
+        reads = tok.state_reads(q, k, v, g, None, s, back)
+        (m, a), (m1, a1) = tok.decay_scale(q, k, v, g, s, back), tok.decayed_scale(q, k, v, g, None, s, back)
+        np.testing.assert_array_equal(m, m1)
+        far = slice(0, 50) if back else slice(10, 60)
+        assert (leak <= 2.0 ** -13 * a)[:, :, far].all()
+        tol = 2.0 ** -8 * (m1 + reads) + 2.0 ** -13 * a1
+        assert (leak > 3 * tol)[:, :, far].mean() > 0.9
+
+
 @pytest.mark.parametrize("lens", [None, [9, 4], [0, 1]])
 def test_gradients_are_the_differences(lens):
     q, k, v, do, g, s, z = _draw(2)
