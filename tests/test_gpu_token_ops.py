@@ -793,3 +793,70 @@ def test_decays_within_the_decayed_bound(d, di, do, lens):
     for got, want, (a, b, c, st, back) in cases:
         floor = 2.0 ** -118 * tok.decay_scale(a, b, c, g, st, back)[1]
         _near_decayed(_flat(got), want, _decayed(a, b, c, g, lens, st, back), do, n, d, floor)
+
+
+SEGMENTS = [
+    # d, in, out, n, lens
+    (16, "bf16", "bf16", 2500, [2500, 1317, 0]), (32, "bf16", "bf16", 2500, [2500, 64, 1]), (16, "f32", "f32", 1500, None),
+    (16, "bf16", "f32", 1500, [1500, 700, 65]), (64, "bf16", "f32", 1500, None), (128, "bf16", "f32", 1000, [1000, 999, 0]),
+    (32, "f32", "bf16", 1500, [3, 1500, 1000]), (128, "f32", "bf16", 1000, None),
+]
+
+
+@pytest.mark.parametrize("case", SEGMENTS, ids=str)
+def test_segments_of_every_width_and_type(case):
+    """Sequences long enough to be cut, whole and ragged; the backward pass where the types allow it."""
+    d, di, do, n, lens = case
+    B, H = 3, 2
+    x = _inputs(28 + d, B, H, 1, n, d, di, names="qkvo", g=[-1e-3, -0.2])
+    s = vdn.make_shape(B, H, 1, n, d, 0, in_dtype=di, out_dtype=do)
+    assert vdn.vdn_decay_attn_workspace_bytes(s) > 0
+    if lens:
+        _poison(x, lens, "qkvo")
+    o, s1 = _attn(s, x, lens)
+    q, k, v, do_ = (_flat(x[c]) for c in "qkvo")
+    g, s0, z = _np(x["g"]), _np(x["s"]), _np(x["z"])
+    ref, ref_s = tok.decay_attn(q, k, v, g, lens, s0)
+    keep = np.isfinite(ref)
+    cases = [(o, ref, lambda: (q, k, v, s0, False))]
+    _state_near(_np(s1), ref_s)
+    if di == do:
+        assert vdn.vdn_decay_attn_backward_workspace_bytes(s) > 0
+        out, ds = _backward(s, x, lens)
+        *refs, ref_ds = tok.decay_attn_backward(q, k, v, g, do_, lens, s0, z)
+        tr = lambda t: np.swapaxes(t, -1, -2)  # noqa: E731
+        cases += list(zip(out, refs, [lambda: (do_, v, k, tr(s0), False), lambda: (v, do_, q, tr(z), True),
+                                      lambda: (k, q, do_, z, True)]))
+        _state_near(_np(ds), ref_ds)
+    q, k, v, do_ = (np.where(keep, y, 0.0) for y in (q, k, v, do_))
+    for got, want, args in cases:
+        a, b, c, st, back = args()
+        _near_decayed(_flat(got), want, _decayed(a, b, c, g, lens, st, back), do, n, d, 0.0)
+        assert (_flat(got)[~keep] == MARK).all()
+
+
+@pytest.mark.parametrize("d", [32, 128])
+def test_steep_heads_in_segments(d):
+    """Cut sequences of heads that forget within a chunk, ragged, in the form with two powers and in the other."""
+    g = [-0.99, -1.38, -1.42, -3.0]
+    n, lens = 2500, [2500, 1331]
+    x = _inputs(29, 2, len(g), 1, n, d, "bf16", names="qkvo", g=g)
+    s = vdn.make_shape(2, len(g), 1, n, d, 0)
+    assert vdn.vdn_decay_attn_workspace_bytes(s) > 0
+    _poison(x, lens, "qkvo")
+    o, s1 = _attn(s, x, lens)
+    out, ds = _backward(s, x, lens)
+    q, k, v, do = (_flat(x[c]) for c in "qkvo")
+    g, s0, z = _np(x["g"]), _np(x["s"]), _np(x["z"])
+    ref, ref_s = tok.decay_attn(q, k, v, g, lens, s0)
+    *refs, ref_ds = tok.decay_attn_backward(q, k, v, g, do, lens, s0, z)
+    keep = np.isfinite(ref)
+    q, k, v, do = (np.where(keep, y, 0.0) for y in (q, k, v, do))
+    tr = lambda t: np.swapaxes(t, -1, -2)  # noqa: E731
+    for got, want, (a, b, c, st, back) in zip([o, *out], [ref, *refs], [
+            (q, k, v, s0, False), (do, v, k, tr(s0), False), (v, do, q, tr(z), True), (k, q, do, z, True)]):
+        floor = 2.0 ** -118 * tok.decay_scale(a, b, c, g, st, back)[1]
+        _near_decayed(_flat(got), want, _decayed(a, b, c, g, lens, st, back), "bf16", n, d, floor)
+        assert (_flat(got)[~keep] == MARK).all()
+    _state_near(_np(s1), ref_s)
+    _state_near(_np(ds), ref_ds)
