@@ -342,6 +342,15 @@ def _raw(t, dev, name):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+def _word(t, dev):
+    """The pointer of info: one int32 on the current device (None for None, an int as it is)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype != torch.int32 or t.numel() < 1 or t.get_device() != dev:
+        _bad(f"info is {t.dtype} {tuple(t.shape)}, not an int32 word on the current CUDA device")
+    return t.data_ptr()
+
+
 def _device():
     return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
 
@@ -420,7 +429,7 @@ def vdn_decay_attn(s, Q, K, V, log_decay, lens, S_in, O, S_out, workspace, info=
         ctypes.byref(s), _arg(Q, ti, x, dev, "Q"), _arg(K, ti, x, dev, "K"), _arg(V, ti, x, dev, "V"),
         _arg(log_decay, f, (s.H,), dev, "log_decay"), _arg(lens, torch.int32, (s.B,), dev, "lens"),
         _arg(S_in, f, st, dev, "S_in"), _arg(O, to, x, dev, "O"), _arg(S_out, f, st, dev, "S_out"), ws, n,
-        _raw(info, dev, "info")[0], _on(stream, dev)))
+        _word(info, dev), _on(stream, dev)))
 
 
 def vdn_decay_attn_backward(s, Q, K, V, log_decay, lens, S_in, dO, dS_out, dQ, dK, dV, dS_in, workspace, info=None,
@@ -435,7 +444,7 @@ def vdn_decay_attn_backward(s, Q, K, V, log_decay, lens, S_in, dO, dS_out, dQ, d
         _arg(log_decay, f, (s.H,), dev, "log_decay"), _arg(lens, torch.int32, (s.B,), dev, "lens"),
         _arg(S_in, f, st, dev, "S_in"), _arg(dO, ti, x, dev, "dO"), _arg(dS_out, f, st, dev, "dS_out"),
         _arg(dQ, ti, x, dev, "dQ"), _arg(dK, ti, x, dev, "dK"), _arg(dV, ti, x, dev, "dV"), _arg(dS_in, f, st, dev, "dS_in"),
-        ws, n, _raw(info, dev, "info")[0], _on(stream, dev)))
+        ws, n, _word(info, dev), _on(stream, dev)))
 
 
 def vdn_decay_step(s, Q, K, V, log_decay, active, S_in, O, S_out, stream=None):

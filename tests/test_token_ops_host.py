@@ -304,3 +304,17 @@ def test_rotary_of_no_tokens(L, kw, grid):
     shape = (s.B, s.H, s.T, s.U, s.dk)
     x = torch.empty(shape, dtype=torch.bfloat16)
     assert vdn._rows(x, shape, torch.bfloat16, -1, "X")[0] == 0
+
+
+def test_info_is_a_word():
+    """The kernels write 32 bits there: smaller and other words are refused, no word at all is none."""
+    import torch
+    assert vdn._word(None, -1) is None and vdn._word(4096, -1) == 4096
+    t = torch.zeros(2, dtype=torch.int32)
+    assert vdn._word(t, -1) == t.data_ptr() and vdn._word(t[1:], -1) == t.data_ptr() + 4
+    for bad in (torch.zeros(1, dtype=torch.uint8), torch.zeros(1), torch.zeros(1, dtype=torch.int64),
+                torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int16)):
+        with pytest.raises(vdn.VdnError, match="info"):
+            vdn._word(bad, -1)
+    with pytest.raises(vdn.VdnError, match="info"):
+        vdn._word(t, 0)  # a host tensor
