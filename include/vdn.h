@@ -465,7 +465,9 @@ typedef struct {
  * Rotates (or copies) n_io tensors, 1 to 3, in one launch.
  * Errors: VDN_ERR_INVALID for axes that do not fit, a grid that is not U
  * tokens, strides as above, a non-positive or non-finite theta, a non-finite
- * scale; VDN_ERR_UNSUPPORTED for B > 65535 or n_io * H > 65535.
+ * scale, a pair of more than 1e6 turns a position, a frame0 beyond its limits, a
+ * y that is another tensor of the call; VDN_ERR_UNSUPPORTED for B > 65535 or
+ * n_io * H > 65535.
  */
 vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_rotary_io *io,
                       int32_t n_io, vdn_stream_t stream);
@@ -486,8 +488,8 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
  *      [B,H,dv,dk] float32 or NULL (zero).
  * Out: O [B,H,T,U,dv] (out_dtype); S_out [B,H,dv,dk] float32 or NULL: the state
  *      behind the last token (S_in for an empty sequence); may be S_in.
- * Values have to be finite: one that is not spoils its sequence's outputs from
- * the start of its 64-token chunk on.
+ * Values have to be finite: one that is not spoils the outputs of its (batch,
+ * head) from the start of its 64-token chunk on, and S_out.
  * info: optional, as for vdn_frame_grams.
  * workspace: at least vdn_decay_attn_workspace_bytes(s) bytes (0 for short
  * sequences: it may then be NULL), 256-byte aligned, its contents undefined
@@ -519,6 +521,8 @@ vdn_status vdn_decay_attn(const vdn_shape *s, const void *Q, const void *K, cons
  *      are not used), dS_out [B,H,dv,dk] float32 or NULL.
  * Out: dQ, dK, dV [B,H,T,U,d] (in_dtype; left as they were behind a sequence's
  *      end), dS_in [B,H,dv,dk] float32 or NULL. No output may be an input.
+ * A value that is not finite spoils of its (batch, head) dQ from the start of its
+ * 64-token chunk on, dK and dV up to that chunk's end, and dS_in.
  */
 size_t vdn_decay_attn_backward_workspace_bytes(const vdn_shape *s);
 vdn_status vdn_decay_attn_backward(const vdn_shape *s, const void *Q, const void *K, const void *V,

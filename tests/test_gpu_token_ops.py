@@ -860,3 +860,23 @@ def test_steep_heads_in_segments(d):
         assert (_flat(got)[~keep] == MARK).all()
     _state_near(_np(s1), ref_s)
     _state_near(_np(ds), ref_ds)
+
+
+@pytest.mark.parametrize("n,at", [(200, 100), (2500, 1500)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["q", "k", "v", "o"])
+def test_how_far_a_nan_reaches(name, dt, n, at):
+    """One value that is no number: the other heads, and of its own the chunks on the far side of either
+    walk, come out as without it."""
+    x = _inputs(30, 2, 2, 1, n, 64, dt, names="qkvo", g=[-0.01, -1.2])
+    s = vdn.make_shape(2, 2, 1, n, 64, 0, in_dtype=dt)
+    clean, (want, _) = _attn(s, x)[0], _backward(s, x)
+    y = {**x, name: x[name].clone()}
+    for h in range(2):
+        y[name][1, h, 0, at, 5] = float("nan")
+    o, (got, _) = _attn(s, y)[0], _backward(s, y)
+    lo, hi = at // 64 * 64, at // 64 * 64 + 64
+    for a, b, back in ((o, clean, False), (got[0], want[0], False), (got[1], want[1], True), (got[2], want[2], True)):
+        assert torch.equal(a[0], b[0])
+        far = slice(hi, n) if back else slice(0, lo)
+        assert torch.equal(a[1][..., far, :], b[1][..., far, :])
