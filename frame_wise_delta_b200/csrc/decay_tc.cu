@@ -20,39 +20,43 @@
 // Four products per chunk, all with 128 TMEM lanes:
 //   SC[i][j]  = Q K^T                 A = Q, B = K (K-major tiles as TMA brings them; rows 64.. unused)
 //   U[v][k]   = (w V)^T K             A = the weighted values in TMEM, B = K (MN-major)
-//   O[v][i]   = X Q^T + (w V)^T P^T   A = l^n X as bf16 in TMEM, B = Q; A = the weighted values (steep:
-//                                     V, MN-major), B = P = the masked SC as bf16, in shared memory
+//   O[v][i]   = X Q^T + (w V)^T P^T   A = l^n X in TMEM, B = Q; A = the weighted values (steep: V,
+//                                     MN-major), B = P = the masked SC, in shared memory
 // The state stays in registers in float32 and is written to TMEM once per chunk, so it never passes
 // through shared memory; the outputs come transposed (lane = channel) and leave through a swizzled
 // staging tile by TMA. The weighted values enter U as three bf16 parts (2^-24 together): two would
-// leave 3e-6 in the float32 state. P and the copy of the state that the outputs read are rounded to
-// bf16: each adds an error of the size of the output's own rounding to its share of the output (the
-// sum is 1.4 times the rounding's alone), and a second part of the state would cost a quarter of the
-// chunk's instructions.
+// leave 3e-6 in the float32 state. P, and the copy of the state that the outputs read, are two bf16 parts
+// each (2^-17), the weighted values beside P too, so that a bf16 output is off by its own rounding and
+// little else. With one part of P and of the state it was off by 1.41 times that, more in small cases, at 24
+// us against 25 (prompts below), 83 against 92 (ragged), 905 against 945 (long), 434 against 470 (gradients).
 //
 // One CTA of 32 warps walks one segment of one (operator, batch, head):
 //   warps 0, 1  : scores SC -> P (TMEM lanes 0..63)
 //   warp 2      : TMA loads, the products U
 //   warp 3      : TMEM allocation, the products SC and O
-//   warps 4..19 : the state: lane = value channel (warp % 4), column quarter (warp - 4) / 4
+//   warps 4..19 : the state: lane = value channel (warp % 4), 32 key channels from 32 ((warp - 4) / 4)
 //   warps 20..27: the weighted values: 32 channels (warp % 4), half of them (warp - 20) / 4
 //   warps 28..31: the outputs
 // Many warps with little each: every role is a chain of dependent steps on the way from one chunk
 // to the next, so it is the length of a warp's share that counts.
 //
-// What bounds it: a chunk costs the tensor pipe 1500 cycles at d = 128 (900 at d <= 64, where half of the
-// lanes are idle), and the warps together about 7000 instructions, in chains of TMEM reads, waits and
-// products that take 2000 to 2700 cycles from one chunk to the next. Measured at d = 128 in bf16:
-// 4 x 24 heads of 512 tokens 24 us (8 chunks each, 1.5 us a chunk and the start); 24 heads of 102 816
-// tokens 0.68 ms alone (pass for the segments' states 0.22 ms, join 0.01, walk 0.45; 2.5 GB in and out, 3.4
-// GB moved, 5.0 TB/s) and 0.79 to 0.89 ms one after another, when they draw 995 W and the clock falls from
-// 1965 to 1400 MHz, so that it is the energy of a chunk that counts; the gradients of 20 160 tokens 0.33 ms
-// alone, 0.40 in a row.
-// At d = 64, 8 x 16 ragged heads of up to 4099 tokens 82 us, the longest walk's 65 chunks.
-// Tried at equal or less speed: the state and the outputs in two TMEM buffers at d = 64 (85 us, with two
-// output tiles in shared memory 90), P by the warps of the other half of the lanes at d = 64 (84 us), outputs
-// by the state's warps (10 % slower), the scores issued by P's warp, one warp for all products in a fixed
-// order (2 % slower), three stages of loads instead of four (1 %).
+// What bounds it: 8000 instructions of all warps a chunk, in chains of TMEM reads, waits and products that
+// take 2200 to 2900 cycles from one chunk to the next, and the code's size: the loops of the roles together
+// are more than the instruction caches hold, so P's blocks are rolled at d = 128 (unrolled 12 % slower in
+// long sequences; at d = 64, where half of the warps are idle, unrolled is 4 % faster) and masks are selects
+// by bit (as words built for pairs of columns: 9 % slower). Leaving out the second parts' products alone
+// changes 0 to 4 %. Measured at d = 128 in bf16: 4 x 24 heads of 512 tokens 25 us (8 chunks each); 24 heads of
+// 102 816 tokens 0.82 to 0.95 ms one after another (2.5 GB in and out, 3.4 GB moved), when they draw 995 W
+// and the clock falls, so that it is the energy of a chunk that counts; the gradients of 20 160 tokens 0.43
+// to 0.47 ms. At d = 64, 8 x 16 ragged heads of up to 4099 tokens 92 us, the longest walk's 65 chunks. Steep
+// heads throughout: 138 us there, 1.04 ms for the long sequences.
+// Tried at equal or less speed: scores and values as tf32 beside P (no splitting, but the values once more
+// and one buffer of them: 103 us against 105 at d = 64 then, equal at d = 128); P by the warps of the
+// other half of the lanes at d = 64, beside the issuing warps (137 us against 105), or those on the busy half
+// (150); two buffers of scores at d = 64 (equal); loads of the scores ahead (12 % slower, code's size); masks
+// kept in registers (20 % slower); the state and the outputs in two TMEM buffers at d = 64 (2 %), with two
+// output tiles in shared memory (9 %); outputs by the state's warps (10 %), the scores issued by P's warp,
+// one warp for all products in a fixed order (2 %).
 // SUMS: only what a segment adds to the state (from zero), for the walk's later segments.
 // Every wait is bounded.
 #include <cudaTypedefs.h>
@@ -75,21 +79,25 @@ struct Cfg {
   static constexpr uint32_t kTile = kPanels * kPanel;
   static constexpr uint32_t kOffK = SUMS ? 0 : kTile, kOffV = kOffK + kTile;  // in a stage, behind Q
   static constexpr uint32_t kStageBytes = kOffV + kTile;
-  static constexpr int kStages = !SUMS && DP == 128 ? 4 : 6;
+  static constexpr int kStages = !SUMS && DP == 128 ? 3 : 6;
   // shared memory, from a 1024-byte aligned base; a 128-row operand reads
   // 8 KB past its 64-row tile, which the next tile or P covers
   static constexpr uint32_t kOffP = kStages * kStageBytes;
-  static constexpr uint32_t kOffO = kOffP + (SUMS ? 0 : 2 * kPanel);  // two P, an output tile
-  static constexpr uint32_t kOffTab = kOffO + (SUMS ? 0 : kTile);
+  static constexpr uint32_t kOffO = kOffP + (SUMS ? 0 : 4 * kPanel);  // two P of two parts, an output tile
+  // the weighted values' third part lies in shared memory where TMEM has no room for it
+  static constexpr bool kLow = !SUMS && DP == 128;
+  static constexpr uint32_t kOffLow = kOffO + (SUMS ? 0 : kTile), kLowBytes = 2 * kPanel;
+  static constexpr uint32_t kOffTab = kOffLow + (kLow ? 2 * kLowBytes : 0);
   static constexpr uint32_t kTabFloats = 2 * 2 * kC + 72 + 8 + 16;  // w, f per set; l^n; carries and 2^c, 2^-c; l^-n
   static constexpr uint32_t kOffBar = kOffTab + 4 * kTabFloats;
   static constexpr uint32_t kBars = 2 * kStages + 14;
   static_assert(kBars <= 32, "a lane each");
   static constexpr size_t kSmem = 1024 + kOffBar + 8 * kBars + 16;
+  static constexpr int kParts = DP / 32;  // of the state, 32 key channels each
   // TMEM columns
-  static constexpr uint32_t kX = 0, kU = DP / 2, kO = kU + DP, kSC = kO + kC, kVT = kSC + kC;
-  static constexpr uint32_t kVTCols = 3 * kC / 2;  // of each of two buffers
-  static_assert(kVT + 2 * kVTCols <= kTmemCols, "TMEM");
+  static constexpr uint32_t kX = 0, kXLow = DP / 2, kU = DP, kO = kU + DP, kSC = kO + kC, kVT = kSC + kC;
+  static constexpr uint32_t kVTCols = (kLow ? 2 : 3) * kC / 2;  // of each of two buffers
+  static_assert(SUMS || kVT + 2 * kVTCols <= kTmemCols, "TMEM");
   // SUMS: two buffers of U as well (from column 0)
   static constexpr uint32_t kVT2 = 2 * DP;
   static_assert(kVT2 + 2 * kVTCols <= kTmemCols, "TMEM");
@@ -186,9 +194,12 @@ __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
   return __byte_perm(a, b, 0x7632);
 }
 
-// Bits x and x + 1 of m as masks of the halves of a word.
-__device__ __forceinline__ uint32_t pair_mask(uint32_t m, int x) {
-  return __byte_perm((uint32_t)((int)(m << (31 - x)) >> 31), (uint32_t)((int)(m << (30 - x)) >> 31), 0x5410);
+// x as two bf16 parts, 2^-17 of it left over: the first, and the second in `low`.
+__device__ __forceinline__ uint32_t split_bf16(float2 x, uint32_t &low) {
+  const uint32_t high = as_u32(__floats2bfloat162_rn(x.x, x.y));
+  x = __ffma2_rn(unpack2(high), make_float2(-1.f, -1.f), x);
+  low = as_u32(__floats2bfloat162_rn(x.x, x.y));
+  return high;
 }
 
 // Four transposed 8 x 8 bf16 matrices (lane l: the address of row l % 8 of
@@ -198,6 +209,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t &x, uint32_t &y, uin
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
                : "r"(a)
+               : "memory");
+}
+// The other way round (stsm4t), and rows as they are (stsm4).
+__device__ __forceinline__ void stsm4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
 }
 __device__ __forceinline__ void stsm4t(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -262,18 +278,12 @@ __device__ __forceinline__ void tmem_ld_frag_wait(float (&v)[32]) {
                : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // A steep head: each valid row of Q (up to `last`) takes the power of two in its decay; 16-byte pieces,
 // two a thread. pw: l^n. A call of its own: within the state's loop its registers and instructions cost
 // the other heads 3 to 5 % (24 heads of 102 816 tokens, d = 128), by P's warps even the steep ones more
 // (8 x 16 heads of 4099 tokens, d = 64: 147 us against 136).
-__device__ __noinline__ void scale_q(uint32_t tile, uint32_t pw, int piece, int threads, int last, int back) {
-#pragma unroll
-  for (int x = 0; x < 2; ++x, piece += threads) {
+__device__ __noinline__ void scale_q(uint32_t tile, uint32_t pw, int piece, int threads, int each, int last, int back) {
+  for (int x = 0; x < each; ++x, piece += threads) {
     const int row = (piece >> 3) & (kC - 1);
     if (row <= last) {
       const uint32_t a = tile + 16 * piece;
@@ -311,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // p_ready; kv_ok: the values are there, U has been read; qx_ok: the state is there, O has been read
     const int n = r < 0              ? (lane < S || SUMS ? 1 : 2)
                   : r >= 1 && r <= 3 ? 64
-                  : r == 4 || r == 5 ? 6 * DP
-                  : r == 10          ? 5 * DP
+                  : r == 4 || r == 5 ? (F::kParts + 2) * DP
+                  : r == 10          ? (F::kParts + 1) * DP
                   : r == 12          ? 2
                                      : 1;
     if (lane < 2 * S + 13) mbar_init(full0 + 8 * lane, n);
@@ -389,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     carry[4 * set + 2] = __uint_as_float(hi > lo ? __double2uint_rn((l - lo) / ((double)hi - lo) * 4294967295.0) : 0u);
   }
   if (!SUMS)
-    for (uint32_t x = threadIdx.x; x < 2 * kPanel / 16; x += kThreads) sts_u4(smem_a + F::kOffP + 16 * x, 0, 0, 0, 0);
+    for (uint32_t x = threadIdx.x; x < 4 * kPanel / 16; x += kThreads) sts_u4(smem_a + F::kOffP + 16 * x, 0, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -438,12 +448,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint64_t k = mnmaj + stage_off(it) + (F::kOffK >> 4);
         const uint32_t u = tm + (SUMS ? (uint32_t)((it & 1) * DP) : F::kU), vt = vt_of(it);
+        const uint64_t low = kmaj + ((F::kOffLow + (it & 1) * F::kLowBytes) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int part = 2; part >= 0; --part)
 #pragma unroll
-            for (int ks = 0; ks < kC / 16; ++ks)
-              tc_mma_bf16_ts(u, vt + part * (kC / 2) + 8 * ks, k + ks * (2048 >> 4), id_u, part < 2 || ks > 0 ? 1u : 0u);
+            for (int ks = 0; ks < kC / 16; ++ks) {
+              if (F::kLow && part == 2)
+                tc_mma_bf16(u, low + ks * (32 >> 4), k + ks * (2048 >> 4), id_u, ks > 0 ? 1u : 0u);
+              else
+                tc_mma_bf16_ts(u, vt + part * (kC / 2) + 8 * ks, k + ks * (2048 >> 4), id_u, part < 2 || ks > 0 ? 1u : 0u);
+            }
           tc_commit(kv_full + 8 * buf(it));
           tc_commit(empty(it));
         }
@@ -499,9 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t q = kmaj + stage_off(it);
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < DP / 16; ++ks)
-            tc_mma_bf16_ts(tm + F::kO, tm + F::kX + 8 * ks, q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4), id_sc,
-                           ks > 0 ? 1u : 0u);
+          for (int part = 1; part >= 0; --part)
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks)
+              tc_mma_bf16_ts(tm + F::kO, tm + (part ? F::kXLow : F::kX) + 8 * ks,
+                             q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4), id_sc, part == 0 || ks > 0 ? 1u : 0u);
           tc_commit(qx_done);
         }
         __syncwarp();
@@ -510,20 +527,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait(p_ready + 8 * (it & 1), phase(it), abort) && warp_wait(kv_ok + 8 * (it & 1), phase(it), abort);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t pb = dp + (it & 1) * (kPanel >> 4);
+        const uint64_t pb = dp + (it & 1) * (2 * kPanel >> 4), pl = pb + (kPanel >> 4);
         const uint64_t v = mnmaj + stage_off(it) + (F::kOffV >> 4);
         const uint32_t vt = vt_of(it);
         if (elect_one()) {
           if (steep) {
 #pragma unroll
-            for (int ks = 0; ks < kC / 16; ++ks)
-              tc_mma_bf16(tm + F::kO, v + ks * (2048 >> 4), pb + ks * (32 >> 4), id_pv, 1u);
-          } else {
-#pragma unroll
             for (int part = 1; part >= 0; --part)
 #pragma unroll
               for (int ks = 0; ks < kC / 16; ++ks)
-                tc_mma_bf16_ts(tm + F::kO, vt + part * (kC / 2) + 8 * ks, pb + ks * (32 >> 4), id_sc, 1u);
+                tc_mma_bf16(tm + F::kO, v + ks * (2048 >> 4), (part ? pl : pb) + ks * (32 >> 4), id_pv, 1u);
+          } else {
+            // values and scores in two parts each, but for the product of the second ones
+#pragma unroll
+            for (int part = 2; part >= 0; --part)
+#pragma unroll
+              for (int ks = 0; ks < kC / 16; ++ks)
+                tc_mma_bf16_ts(tm + F::kO, vt + (part == 1 ? kC / 2 : 0) + 8 * ks, (part == 2 ? pl : pb) + ks * (32 >> 4), id_sc, 1u);
           }
           tc_commit(pv_done + 8 * (it & 1));
           tc_commit(empty(it));
@@ -547,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = pinned(warp * 32 + lane);  // addresses made here, not kept
         const int c = chunk_at(it), n = rows_of(c);
         const uint32_t t = tab_a + set_of(c) * (2 * kC * 4), pw_a = tab_a + 4 * 2 * 2 * kC;
-        const uint32_t row = smem_a + F::kOffP + (it & 1) * kPanel + i * 128;
+        const uint32_t row = smem_a + F::kOffP + (it & 1) * 2 * kPanel + i * 128;
         // the columns this row takes
         const uint64_t upto = (2ull << i) - 1, rows = n < kC ? (1ull << n) - 1 : ~0ull;
         const uint64_t mask = back ? rows & ~(upto >> 1) : upto;
@@ -557,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-#pragma unroll
+#pragma unroll(DP == 128 ? 2 : 4)  // see the code's size above
         for (int b = 0; b < 4; ++b) {  // 16 columns
           if ((b >> 1) == skip) continue;
           float v[16];
@@ -580,16 +600,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const bool all = (b >> 1) != warp && n == kC;  // the block lies within the mask
           const uint32_t m = (uint32_t)(mask >> (16 * b));
+          if (!all) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) v[x] = m >> x & 1 ? v[x] : 0.f;
+          }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            uint32_t pk[4];
+            uint32_t pk[4], pl[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pk[e] = pack_bf16(v[8 * x + 2 * e], v[8 * x + 2 * e + 1]);
-            if (!all) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) pk[e] &= pair_mask(m, 8 * x + 2 * e);
-            }
-            sts_u4(row + (((2 * b + x) ^ (i & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+            for (int e = 0; e < 4; ++e) pk[e] = split_bf16(make_float2(v[8 * x + 2 * e], v[8 * x + 2 * e + 1]), pl[e]);
+            const uint32_t to = row + (((2 * b + x) ^ (i & 7)) << 4);
+            sts_u4(to, pk[0], pk[1], pk[2], pk[3]);
+            sts_u4(to + kPanel, pl[0], pl[1], pl[2], pl[3]);
           }
         }
         fence_proxy_async_smem();
@@ -599,10 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 20) {
     // --------------------------------------------------------- the state
     const int sub = warp & 3, part = (warp - 4) >> 2;
-    const int r = sub * 32 + lane, c0 = part * (DP / 4);  // value channel, first key channel
+    const int r = sub * 32 + lane, c0 = part * 32;  // value channel, first key channel
     const uint32_t lanes = (uint32_t)(sub * 32) << 16;
-    if (sub * 32 < DP) {
-      float2 X[DP / 8];
+    if (sub * 32 < DP && part < F::kParts) {
+      float2 X[16];
       const float *src = nullptr;
       bool tr = false;
       if (!SUMS) {
@@ -612,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int sr = tr ? 1 : d, sc = tr ? d : 1;  // strides of a state's row and column
       const float up = lds_f(tab_a + 4 * (2 * 2 * kC + 72 + 3));
 #pragma unroll
-      for (int x = 0; x < DP / 8; ++x) {
+      for (int x = 0; x < 16; ++x) {
         X[x] = make_float2(0.f, 0.f);
         if (src && r < d && c0 + 2 * x < d) {
           const float *y = src + r * sr + (c0 + 2 * x) * sc;
@@ -623,16 +645,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float lx = steep ? 1.f : lds_f(tab_a + 4 * (2 * 2 * kC + 72 + 4 * set_of(chunk_at(it))));
         const float2 sc = make_float2(lx, lx);
 #pragma unroll
-        for (int b = 0; b < DP / 32; ++b) {
-          uint32_t y[4];
+        for (int b = 0; b < 4; ++b) {
+          uint32_t y[4], low[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             float2 z = X[4 * b + x];
             asm volatile("" : "+f"(z.x), "+f"(z.y));  // piece by piece: fewer registers at once
-            z = __fmul2_rn(z, sc);
-            y[x] = as_u32(__floats2bfloat162_rn(z.x, z.y));
+            y[x] = split_bf16(__fmul2_rn(z, sc), low[x]);
           }
-          tmem_st4(tmem + lanes + F::kX + part * (DP / 8) + 4 * b, y);
+          tmem_st4(tmem + lanes + F::kX + part * 16 + 4 * b, y);
+          tmem_st4(tmem + lanes + F::kXLow + part * 16 + 4 * b, low);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -654,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = warp_wait(p_ready + 8 * buf(it), phase(it), abort) &&
                  warp_wait(full0 + 8 * s, (uint32_t)((it / F::kStages) & 1), abort);
             if (!ok) break;
-            scale_q(smem_a + s * F::kStageBytes, tab_a + 4 * (2 * 2 * kC), part * DP + r, 4 * DP, rows_of(chunk_at(it)) - 1, back);
+            scale_q(smem_a + s * F::kStageBytes, tab_a + 4 * (2 * 2 * kC), part * DP + r, F::kParts * DP, 8 / F::kParts, rows_of(chunk_at(it)) - 1, back);
           }
           mbar_arrive(qx_ok);
         }
@@ -667,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < DP / 32; ++b) {
+        for (int b = 0; b < 4; ++b) {
           float u[8];
           tmem_ld8(u_at(it) + lanes + c0 + 8 * b, u);
 #pragma unroll
@@ -681,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) fail(abort, p.info);
       // where it goes is found anew: kept over the loop, it would cost registers
-      const int tid = pinned((int)threadIdx.x), blk = pinned((int)blockIdx.x), r1 = tid & 127, c1 = ((tid >> 7) - 1) * (DP / 4);
+      const int tid = pinned((int)threadIdx.x), blk = pinned((int)blockIdx.x), r1 = tid & 127, c1 = ((tid >> 7) - 1) * 32;
       const DecayWork w1 = decay_work(p, blk, SUMS);
       const DecayOp &op1 = p.op[w1.op];
       float *dst = nullptr;
@@ -692,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float down = lds_f(tab_a + 4 * (2 * 2 * kC + 72 + 7));
       if (dst && r1 < p.d) {
 #pragma unroll
-        for (int x = 0; x < DP / 4; x += 4)
+        for (int x = 0; x < 32; x += 4)
           if (c1 + x < p.d)
             *reinterpret_cast<float4 *>(dst + r1 * p.d + c1 + x) =
                 make_float4(down * X[x / 2].x, down * X[x / 2].y, down * X[x / 2 + 1].x, down * X[x / 2 + 1].y);
@@ -758,7 +780,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t to = vt_at(it) + lanes + ((uint32_t)(16 * h) << 16) + 16 * half;
           tmem_st_frag(to, &x[8 * half]);
           tmem_st_frag(to + kC / 2, m);
-          tmem_st_frag(to + kC, l);
+          if (F::kLow) {
+            // rows of channels, 8 tokens (16 bytes) a piece
+            const uint32_t row = smem_a + F::kOffLow + buf(it) * F::kLowBytes +
+                                 (uint32_t)(sub * 32 + 16 * h + (lane & 15)) * 128u;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              stsm4(row + (((uint32_t)(4 * half + 2 * e + (lane >> 4)) ^ (uint32_t)(lane & 7)) << 4), l[4 * e], l[4 * e + 1],
+                    l[4 * e + 2], l[4 * e + 3]);
+          } else {
+            tmem_st_frag(to + kC, l);
+          }
         }
         if (n < kC) {
           // what lies behind the sequence's end meets zeros in the products:
@@ -771,8 +803,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             sts_u4(a, 0, 0, 0, 0);
             sts_u4(a - F::kOffV + F::kOffK, 0, 0, 0, 0);
           }
-          fence_proxy_async_smem();
         }
+        if (F::kLow || n < kC) fence_proxy_async_smem();
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(kv_ok + 8 * buf(it));

@@ -496,8 +496,9 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
  * before and after; calls that may run at the same time need one each.
  * Precision: float32 sums and state. With bf16 inputs and output the products
  * run on the tensor cores: the decayed values enter the state as three bf16
- * parts (2^-24 relative); the scores, and the copy of the state that the
- * outputs of a chunk read, are rounded to bf16. A decay below 2^-126 (of the
+ * parts (2^-24 relative); they, the scores, and the copy of the state that the
+ * outputs of a chunk read, enter the outputs as two (2^-15), so that what an
+ * output is off by is its own rounding. A decay below 2^-126 (of the
  * state up to a token, or of one token up to another of its chunk) counts as 0. Range with bf16 inputs
  * and output: heads with -0.975 <= log_decay < 0 carry a factor 2^c inside, c =
  * -46.2 log_decay; states and sums there (of |q . k| |v|, and of |v| |k|) have to

@@ -880,3 +880,34 @@ def test_how_far_a_nan_reaches(name, dt, n, at):
         assert torch.equal(a[0], b[0])
         far = slice(hi, n) if back else slice(0, lo)
         assert torch.equal(a[1][..., far, :], b[1][..., far, :])
+
+
+@pytest.mark.parametrize("d,n,lens", [(16, 1, None), (128, 1, None), (16, 256, [256, 0]), (64, 70, None), (32, 300, [300, 129]),
+                                      (128, 300, [300, 200]), (128, 1500, None), (64, 1500, [1500, 1337])], ids=str)
+def test_bf16_outputs_are_off_by_their_own_rounding(d, n, lens):
+    """Scores and the state's copy enter in two bf16 parts (2^-16 each), the weighted values in two that are
+    cut off, and the product of the second parts is left out: 2^-14 of M_i and R_i together. The float32 sums
+    of d + 64 terms and a few chunks' states: 2^-15 of A_i. The output's rounding, half a step, is what
+    remains: the error's norm is that of the rounded definition's to 2 %, (2^-14 / 2^-9.2)^2 < 0.2 % of its
+    square and twice the chance of a rounding that falls the other way."""
+    g = [0.0, -1e-4, -0.01, -0.1, -0.5, -0.95, -1.2, -3.0]
+    B = 1 if lens is None else 2
+    x = _inputs(33 + d + n, B, len(g), 1, n, d, "bf16", names="qkvo", g=g)
+    s = vdn.make_shape(B, len(g), 1, n, d, 0)
+    o, _ = _attn(s, x, lens)
+    out, _ = _backward(s, x, lens)
+    q, k, v, do = (_flat(x[c]) for c in "qkvo")
+    s0, z, g = _np(x["s"]), _np(x["z"]), np.array(g, np.float32).astype(np.float64)
+    ref, _ = tok.decay_attn(q, k, v, g, lens, s0)
+    *refs, _ = tok.decay_attn_backward(q, k, v, g, do, lens, s0, z)
+    keep = np.isfinite(ref)
+    q, k, v, do = (np.where(keep, y, 0.0) for y in (q, k, v, do))
+    tr = lambda t: np.swapaxes(t, -1, -2)  # noqa: E731
+    for got, want, (a, b, c, st, back) in zip([o, *out], [ref, *refs], [
+            (q, k, v, s0, False), (do, v, k, tr(s0), False), (v, do, q, tr(z), True), (k, q, do, z, True)]):
+        m, sums, reads = _decayed(a, b, c, g, lens, st, back)
+        off = np.abs(_flat(got) - want)[keep]
+        tol = (2.0 ** -8 * np.abs(want) + 2.0 ** -14 * (m + reads) + 2.0 ** -15 * sums)[keep]
+        assert (off <= tol).all()
+        rounded = _np(torch.from_numpy(np.nan_to_num(want)).to(torch.bfloat16))
+        assert np.linalg.norm(off) <= 1.02 * np.linalg.norm((rounded - want)[keep])
