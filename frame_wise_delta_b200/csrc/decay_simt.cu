@@ -481,11 +481,11 @@ DecaySplit decay_split(long long pairs, long long sums, long long n, int slots, 
   // join. Ragged sequences are half full on average, and the CTAs of short
   // ones leave their place at once: then the longest walk or half of the whole
   // work counts, whichever is more.
-  // A launch and a start cost the tensor-core kernel (1.2 to 2 us a chunk) several
+  // A launch and a start cost the tensor-core kernel (1.4 to 2 us a chunk) several
   // chunks' time, the CUDA-core one (10 us) less than one.
-  // Measured: 24 heads of 102 816 tokens, d = 128: 6 segments 0.85 ms (a single
-  // one would be 1607 chunks of 1.7 us in a row, 2.7 ms); 8 x 16 ragged heads of
-  // up to 4099 tokens, d = 64: a single segment 82 us, two 92 us.
+  // Measured: 24 heads of 102 816 tokens, d = 128: 6 segments 0.82 to 0.95 ms (a single
+  // one would be 1607 chunks of 1.9 us in a row, 3 ms); 8 x 16 ragged heads of
+  // up to 4099 tokens, d = 64: a single segment 92 us, two about 12 % more.
   const long long chunks = n > 0 ? (n + kDecayC - 1) / kDecayC : 1;
   DecaySplit best{1, (int)(chunks * kDecayC), 1};
   if (pairs > 8LL * slots) return best;  // several waves of whole walks

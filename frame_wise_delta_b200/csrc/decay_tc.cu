@@ -40,21 +40,21 @@
 // Many warps with little each: every role is a chain of dependent steps on the way from one chunk
 // to the next, so it is the length of a warp's share that counts.
 //
-// What bounds it: 8000 instructions of all warps a chunk, in chains of TMEM reads, waits and products that
+// What bounds it: 10 000 instructions of all warps a chunk, in chains of TMEM reads, waits and products that
 // take 2200 to 2900 cycles from one chunk to the next, and the code's size: the loops of the roles together
 // are more than the instruction caches hold, so P's blocks are rolled at d = 128 (unrolled 12 % slower in
 // long sequences; at d = 64, where half of the warps are idle, unrolled is 4 % faster) and masks are selects
 // by bit (as words built for pairs of columns: 9 % slower). Leaving out the second parts' products alone
 // changes 0 to 4 %. Measured at d = 128 in bf16: 4 x 24 heads of 512 tokens 25 us (8 chunks each); 24 heads of
-// 102 816 tokens 0.82 to 0.95 ms one after another (2.5 GB in and out, 3.4 GB moved), when they draw 995 W
-// and the clock falls, so that it is the energy of a chunk that counts; the gradients of 20 160 tokens 0.43
-// to 0.47 ms. At d = 64, 8 x 16 ragged heads of up to 4099 tokens 92 us, the longest walk's 65 chunks. Steep
+// 102 816 tokens 0.77 ms alone (pass for the segments' states 0.22 ms, join 0.01, walk 0.54; 2.5 GB in and
+// out, 3.4 GB moved) and 0.82 to 0.95 ms one after another, when they draw 995 W and the clock falls, so that
+// it is the energy of a chunk that counts; the gradients of 20 160 tokens 0.39 ms alone, 0.43 to 0.47 in a row. At d = 64, 8 x 16 ragged heads of up to 4099 tokens 92 us, the longest walk's 65 chunks. Steep
 // heads throughout: 138 us there, 1.04 ms for the long sequences.
 // Tried at equal or less speed: scores and values as tf32 beside P (no splitting, but the values once more
 // and one buffer of them: 103 us against 105 at d = 64 then, equal at d = 128); P by the warps of the
 // other half of the lanes at d = 64, beside the issuing warps (137 us against 105), or those on the busy half
 // (150); two buffers of scores at d = 64 (equal); loads of the scores ahead (12 % slower, code's size); masks
-// kept in registers (20 % slower); the state and the outputs in two TMEM buffers at d = 64 (2 %), with two
+// kept in registers (7 %); the state and the outputs in two TMEM buffers at d = 64 (2 %), with two
 // output tiles in shared memory (9 %); outputs by the state's warps (10 %), the scores issued by P's warp,
 // one warp for all products in a fixed order (2 %).
 // SUMS: only what a segment adds to the state (from zero), for the walk's later segments.
@@ -278,8 +278,8 @@ __device__ __forceinline__ void tmem_ld_frag_wait(float (&v)[32]) {
                : "memory");
 }
 
-// A steep head: each valid row of Q (up to `last`) takes the power of two in its decay; 16-byte pieces,
-// two a thread. pw: l^n. A call of its own: within the state's loop its registers and instructions cost
+// A steep head: each valid row of Q (up to `last`) takes the power of two in its decay; `each`
+// pieces of 16 bytes a thread. pw: l^n. A call of its own: within the state's loop its registers and instructions cost
 // the other heads 3 to 5 % (24 heads of 102 816 tokens, d = 128), by P's warps even the steep ones more
 // (8 x 16 heads of 4099 tokens, d = 64: 147 us against 136).
 __device__ __noinline__ void scale_q(uint32_t tile, uint32_t pw, int piece, int threads, int each, int last, int back) {
@@ -676,7 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = warp_wait(p_ready + 8 * buf(it), phase(it), abort) &&
                  warp_wait(full0 + 8 * s, (uint32_t)((it / F::kStages) & 1), abort);
             if (!ok) break;
-            scale_q(smem_a + s * F::kStageBytes, tab_a + 4 * (2 * 2 * kC), part * DP + r, F::kParts * DP, 8 / F::kParts, rows_of(chunk_at(it)) - 1, back);
+            scale_q(smem_a + s * F::kStageBytes, tab_a + 4 * (2 * 2 * kC), part * DP + r, F::kParts * DP, 8 / F::kParts,
+                    rows_of(chunk_at(it)) - 1, back);
           }
           mbar_arrive(qx_ok);
         }

@@ -25,7 +25,7 @@
 //
 // Measured: Q and K of 102 816 tokens x 24 heads x 128 channels in bf16, 2.5 GB
 // moved, 0.40 ms (6.3 TB/s, 97 % of a plain copy's rate); Q, K and V of 5040
-// tokens, token-major, in stretches of 8 bytes, 42 us (186 MB, 4.5 TB/s): there
+// tokens, token-major, in stretches of 8 bytes, 40.5 us (186 MB, 4.6 TB/s): there
 // the angles cost about as much as turning five heads. Sixteen tokens in
 // float32 and the like are one launch, 5 us behind 12 us of the caller's.
 #include <cuda_bf16.h>
