@@ -497,13 +497,14 @@ vdn_status vdn_rotary(const vdn_shape *s, const vdn_rotary_args *r, const vdn_ro
  * Precision: float32 sums and state. With bf16 inputs and output the products
  * run on the tensor cores: the decayed values enter the state as three bf16
  * parts (2^-24 relative); they, the scores, and the copy of the state that the
- * outputs of a chunk read, enter the outputs as two (2^-15), so that what an
- * output is off by is its own rounding. A decay below 2^-126 (of the
- * state up to a token, or of one token up to another of its chunk) counts as 0. Range with bf16 inputs
- * and output: heads with -0.975 <= log_decay < 0 carry a factor 2^c inside, c =
- * -46.2 log_decay; states and sums there (of |q . k| |v|, and of |v| |k|) have to
- * stay below 2^(127 - c), 4e24 in the worst head, and values below 2^-57 may lose
- * low bits. Other heads and types have float32's range.
+ * outputs of a chunk read, enter the outputs as two (2^-15), so that an output
+ * is off by its own rounding and little else. A decay below 2^-126 (of the state
+ * up to a token, or of one token up to another of its chunk) counts as 0.
+ * Range with bf16 inputs and output: heads with -0.975 <= log_decay < 0 carry a
+ * factor 2^c inside, c = -46.2 log_decay; states and sums there (of |q . k| |v|,
+ * and of |v| |k|) have to stay below 2^(127 - c), 4e24 in the worst head, and
+ * values below 2^-57 may lose low bits. Other heads and types have float32's
+ * range.
  */
 size_t vdn_decay_attn_workspace_bytes(const vdn_shape *s);
 vdn_status vdn_decay_attn(const vdn_shape *s, const void *Q, const void *K, const void *V,
